@@ -14,6 +14,11 @@
  *                            own scratch memory, for callers that cannot allocate)
  *   moe_elb_accumulate / moe_elb_top_m   the expert lookahead buffer of a speculative draft
  *   moe_bf16_recombine       BF16 values from separately stored exponent / sign-mantissa bytes
+ *   moe_linear               the dense product beside the experts, with bias, activation and
+ *                            residual; moe_linear_backward its gradients
+ *   moe_balance_loss         the router's balance loss and per-expert counts;
+ *   moe_route_backward, moe_combine_backward  gradients of the router logits (gate weights and
+ *                            balance loss) and of the gate weights and expert rows
  *
  * Sources (page, section):
  *   [W] "Who Says Elephants Can't Run: Bringing Large Scale MoE Models into Cloud Scale
@@ -62,7 +67,10 @@ extern "C" {
 enum moe_gate  { MOE_GATE_SOFTMAX_TOPK = 0,   /* softmax over the k chosen logits        */
                  MOE_GATE_SOFTMAX_ALL  = 1 }; /* softmax over all E, then keep the top k */
 enum moe_wtype { MOE_W_INT4 = 0, MOE_W_INT8 = 1, MOE_W_FP16 = 2 };
-enum moe_act   { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SWIGLU = 2 };
+enum moe_act   { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SWIGLU = 2,
+                 MOE_ACT_SILU = 3,            /* z / (1 + exp(-z)): moe_linear only      */
+                 MOE_ACT_GELU = 4 };          /* z Phi(z), exact: moe_linear only        */
+enum moe_dtype { MOE_DT_FP16 = 0, MOE_DT_BF16 = 1, MOE_DT_FP32 = 2 };
 enum moe_path  { MOE_PATH_AUTO = 0,           /* chosen from R, E, K, N                  */
                  MOE_PATH_STREAM = 1,         /* weight-streaming path, 16-row tiles     */
                  MOE_PATH_TILE = 2 };         /* LDS-staged MFMA tile path, 48/64-row tiles */
@@ -419,6 +427,145 @@ int32_t moe_bf16_recombine(const uint8_t* exponents, const uint8_t* sign_mantiss
 int32_t moe_dequant(const void* w_packed, const uint16_t* scales, int32_t wtype,
                     int32_t group_size, int32_t E, int32_t K, int32_t N, uint16_t* w_out,
                     void* stream);
+
+/*
+ * moe_linear -- the dense product beside the experts: router logits, the dense FFN layers and
+ * projections between MoE layers, products with the BF16 weights moe_bf16_recombine restores.
+ *
+ *   z = a w^T + bias;   preact = round(z);   out = round(act(z) + residual)
+ *
+ *   a         16-bit [M, K], row stride lda >= K elements
+ *   w         16-bit [N, K] (a row per output column), row stride ldw >= K
+ *   bias      16-bit [N] or NULL
+ *   residual  16-bit [M, N], row stride ldr >= N, or NULL; may be `out` itself (same pointer, same
+ *             stride, out_dtype == dtype): the residual stream updated in place
+ *   dtype     MOE_DT_FP16 or MOE_DT_BF16: the type of a, w, bias, residual and preact
+ *   act       MOE_ACT_NONE, RELU, SILU or GELU (SWIGLU: MOE_ERR_UNSUPPORTED)
+ *   out       [M, N] of out_dtype (dtype itself, or MOE_DT_FP32, e.g. router logits), row stride
+ *             ldo >= N.  Apart from `residual` no output may overlap an input.
+ *   preact    16-bit [M, N], row stride ldp >= N, or NULL: z, as moe_linear_backward reads it
+ *   ws        workspace of at least moe_linear_workspace_size(M, N, K, lda, ldw) bytes (0 for many
+ *             sizes: NULL allowed then); contents on entry do not matter, and calls that share one
+ *             workspace must not overlap in time
+ *   Sums, bias, activation and residual are fp32; each output is rounded once (nearest even), the
+ *   activation acting on the unrounded z.  A NaN stays a NaN through every activation.
+ *   Any M >= 0, N >= 0, K >= 1.  Rows that do not start on 16 bytes (lda or ldw, or K, not a
+ *   multiple of 8) are first copied into the workspace; other strides cost nothing.
+ * Errors: MOE_ERR_INVALID for a negative size, K < 1, a stride shorter than its row, an unknown
+ * type or activation, a NULL or misaligned pointer (16 bytes; bias 2); MOE_ERR_UNSUPPORTED for
+ * strides, N or K above 2^22, M above 2^28, M * N, M * K or N * K from 2^36, MOE_ACT_SWIGLU, or
+ * out_dtype neither dtype nor MOE_DT_FP32; MOE_ERR_WORKSPACE.
+ */
+int32_t moe_linear(const uint16_t* a, int64_t lda, const uint16_t* w, int64_t ldw,
+                   const uint16_t* bias, const uint16_t* residual, int64_t ldr, int32_t M,
+                   int32_t N, int32_t K, int32_t dtype, int32_t act, void* out, int64_t ldo,
+                   int32_t out_dtype, uint16_t* preact, int64_t ldp, void* ws, size_t ws_bytes,
+                   void* stream);
+size_t moe_linear_workspace_size(int32_t M, int32_t N, int32_t K, int64_t lda, int64_t ldw);
+
+/*
+ * moe_linear_backward -- the gradients of moe_linear.
+ *
+ *   dz = grad_out * act'(preact);   grad_a = dz w;   grad_w = dz^T a;   grad_bias = sum_m dz
+ *
+ *   grad_out   [M, N] of grad_dtype (dtype itself, or MOE_DT_FP32, e.g. moe_route_backward's
+ *              logit gradients), row stride ldg >= N.  The residual's gradient is grad_out itself.
+ *   preact     16-bit [M, N], row stride ldp >= N: what moe_linear wrote; not read (may be NULL)
+ *              with MOE_ACT_NONE.  relu'(0) = 0.
+ *   a, w       as moe_linear's; a is read for grad_w only, w for grad_a only (else may be NULL)
+ *   grad_a     16-bit [M, K] dense, or NULL: not wanted.  grad_w: 16-bit [N, K] dense, or NULL.
+ *   grad_bias  16-bit [N], or NULL
+ *   ws         at least moe_linear_backward_workspace_size(...) bytes, as for moe_linear
+ *   Sums are fp32.  grad_bias sums the unrounded dz.  The products read dz in dtype: a 16-bit
+ *   gradient with MOE_ACT_NONE or RELU is exact there, one through SILU or GELU is rounded once
+ *   more, an fp32 gradient enters as two 16-bit parts (its first 16 bits in bf16, 22 in fp16).
+ *   fp16 has a short range: scale the loss so that dz lies within it, as fp16 training does.
+ *   With M == 0 grad_w and grad_bias, and with N == 0 grad_a, are written as zeros.
+ * Errors: as moe_linear, plus MOE_ERR_INVALID when no gradient is wanted, or for an activation
+ * without preact.
+ */
+int32_t moe_linear_backward(const void* grad_out, int64_t ldg, int32_t grad_dtype,
+                            const uint16_t* preact, int64_t ldp, const uint16_t* a, int64_t lda,
+                            const uint16_t* w, int64_t ldw, int32_t M, int32_t N, int32_t K,
+                            int32_t dtype, int32_t act, uint16_t* grad_a, uint16_t* grad_w,
+                            uint16_t* grad_bias, void* ws, size_t ws_bytes, void* stream);
+size_t moe_linear_backward_workspace_size(int32_t M, int32_t N, int32_t K, int64_t lda, int64_t ldw,
+                                          int64_t ldg, int32_t grad_dtype, int32_t act);
+
+/*
+ * moe_balance_loss -- the router's balance loss, with its counts and mean probabilities.
+ *   For segment s (one packed sequence, or the whole batch) with n_s live tokens:
+ *     counts[s, e] = slots of live tokens routed to expert e
+ *     probs[s, e]  = 1/n_s sum over live t of softmax(logits[t])[e]
+ *     f[s, e]      = E counts[s, e] / (k n_s)
+ *     loss         = coef * mean over segments with n_s > 0 of sum_e f[s, e] probs[s, e]
+ *   (1 * coef for a perfectly balanced routing, up to E / k * coef for a collapsed one.)
+ *
+ *   logits       fp32 [T, E].  -inf (an expert switched off) and NaN have probability 0; a row
+ *                with nothing else has no probability but counts in n_s; +inf gives NaN.
+ *   topk_ids     int32 [T, k] as moe_route_topk writes them; ids outside [0, E) are not counted,
+ *                an id that appears twice in a row counts twice
+ *   active       uint8 [T] or NULL (= all live): a token with 0 (padding, finished) is left out
+ *   seq_offsets  int32 [S + 1] or NULL (then S must be 1: all T tokens): segment s holds tokens
+ *                seq_offsets[s] .. seq_offsets[s+1] - 1; non-decreasing values in [0, T].  Empty
+ *                segments are allowed; tokens before the first or behind the last belong to none.
+ *                (Values outside are clamped, a decreasing pair is an empty segment.)
+ *   loss         fp32 [1] out: 0 when no token is live
+ *   counts       int32 [S, E] out;  probs fp32 [S, E] out (0 for an empty segment);
+ *   tokens       int32 [S] out: n_s
+ *   ws           at least moe_balance_workspace_size(T, E, S) bytes; contents on entry do not
+ *                matter, calls that share one workspace must not overlap in time
+ *   Requires 1 <= E <= 256, 1 <= k <= 8, S >= 1, T >= 0 (MOE_ERR_UNSUPPORTED for S > 2^20,
+ *   T >= 2^28 or T * E >= 2^31).  T == 0 writes zeros.
+ */
+int32_t moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* active,
+                         const int32_t* seq_offsets, int32_t S, int32_t T, int32_t E, int32_t k,
+                         float coef, float* loss, int32_t* counts, float* probs, int32_t* tokens,
+                         void* ws, size_t ws_bytes, void* stream);
+size_t moe_balance_workspace_size(int32_t T, int32_t E, int32_t S);
+
+/*
+ * moe_route_backward -- gradient of the router logits, through the gate weights, the balance
+ * loss, or both in one pass.
+ *   gate weights (grad_w given), u = sum_j grad_w[t,j] topk_w[t,j] over routed slots:
+ *     MOE_GATE_SOFTMAX_TOPK  grad[t, id_j] += topk_w[t,j] (grad_w[t,j] - u)
+ *     MOE_GATE_SOFTMAX_ALL   grad[t, id_j] += topk_w[t,j] grad_w[t,j];  grad[t, e] -= p[t,e] u
+ *   balance loss (counts given), p = softmax(logits[t]), f as in moe_balance_loss:
+ *     grad[t, e] += grad_loss * coef / (S' n_s) * p[t,e] (f[s,e] - sum_e' f[s,e'] p[t,e']),
+ *     S' = segments with tokens, for live tokens of a segment
+ *
+ *   logits, topk_ids, active, seq_offsets, S, T, E, k, coef  as for moe_balance_loss
+ *   topk_w       fp32 [T, k] as moe_route_topk wrote them, or NULL without grad_w
+ *   grad_w       fp32 [T, k] gradient of the gate weights (moe_combine_backward), or NULL; slots
+ *                with an id outside [0, E) are left out
+ *   counts, tokens  what moe_balance_loss wrote, both or neither NULL
+ *   grad_loss    fp32 [1] on the device, or NULL (= 1)
+ *   grad_logits  fp32 [T, E] out: every element is written (a token that is not live gets zeros)
+ * Errors: MOE_ERR_INVALID when neither grad_w nor counts is given, or for grad_w without topk_w.
+ */
+int32_t moe_route_backward(const float* logits, const int32_t* topk_ids, const float* topk_w,
+                           const float* grad_w, const uint8_t* active, const int32_t* seq_offsets,
+                           int32_t S, int32_t T, int32_t E, int32_t k, int32_t gate_mode,
+                           const int32_t* counts, const int32_t* tokens, float coef,
+                           const float* grad_loss, float* grad_logits, void* stream);
+
+/*
+ * moe_combine_backward -- the gradients of moe_unpermute_combine (called with topk_w, on expert
+ * rows the GEMM did not scale: no row_scale).
+ *   grad_w[t, j] = sum_d grad_out[t, d] y_perm[inv_perm[t*k+j], d]
+ *   grad_y[inv_perm[t*k+j], d] = fp16(topk_w[t, j] grad_out[t, d])
+ *   The addend's gradient is grad_out itself.
+ *
+ *   grad_out  fp16 [T, d];  inv_perm int32 [T*k] (moe_permute)
+ *   y_perm    fp16 [R, d], R >= T*k rows; read for grad_w only
+ *   topk_w    fp32 [T, k]; read for grad_y only
+ *   grad_w    fp32 [T, k] out, or NULL: not wanted; a dropped slot (inv_perm outside [0, T*k)) gets 0
+ *   grad_y    fp16 [R, d] out, or NULL; rows no slot points at are left as they were
+ *   Sums are fp32.  Requires 1 <= k <= 8, d % 8 == 0, T < 2^24, and grad_w or grad_y.
+ */
+int32_t moe_combine_backward(const uint16_t* grad_out, const uint16_t* y_perm,
+                             const int32_t* inv_perm, const float* topk_w, int32_t T, int32_t k,
+                             int32_t d, float* grad_w, uint16_t* grad_y, void* stream);
 
 /* ---- host-only helpers (no device needed) ---- */
 

@@ -7,6 +7,7 @@ functions carry the names of the C entry points declared in include/moe_wq.h.
 The library is loaded on first use and a missing or unloadable library raises
 `MoELibraryError`: there is no fallback implementation.
 """
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -31,14 +32,18 @@ __all__ = [
     "moe_decode_layer_noalloc", "MOE_DECODE_SCRATCH_BYTES", "moe_decode_layer_shared",
     "moe_decode_shared_workspace_size",
     "MOE_DECODE_MAX_TOKENS", "MOE_DECODE_MAX_ROWS", "moe_elb_accumulate", "moe_elb_top_m",
-    "moe_bf16_recombine",
+    "moe_bf16_recombine", "ACT_SILU", "ACT_GELU", "DT_FP16", "DT_BF16", "DT_FP32",
+    "moe_linear", "moe_linear_workspace_size", "moe_linear_backward",
+    "moe_linear_backward_workspace_size", "moe_balance_loss", "moe_balance_workspace_size",
+    "moe_route_backward", "moe_combine_backward",
 ]
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, -1, -2, -3
 MOE_ERR_NO_DEVICE, MOE_ERR_HIP = -4, -5
 GATE_TOPK, GATE_ALL = 0, 1
 W_INT4, W_INT8, W_FP16 = 0, 1, 2
-ACT_NONE, ACT_RELU, ACT_SWIGLU = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_SWIGLU, ACT_SILU, ACT_GELU = 0, 1, 2, 3, 4
+DT_FP16, DT_BF16, DT_FP32 = 0, 1, 2
 PATH_AUTO, PATH_STREAM, PATH_TILE = 0, 1, 2
 TILE_AUTO, TILE_64x256, TILE_64x128, TILE_128x128, TILE_48x256, TILE_48x128 = 0, 1, 2, 3, 4, 5
 I2F_TRICK, I2F_NATIVE = 0, 1
@@ -49,6 +54,7 @@ MOE_DECODE_SCRATCH_BYTES = 8 << 20
 
 WTYPES = {"int4": W_INT4, "int8": W_INT8, "fp16": W_FP16}
 ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "swiglu": ACT_SWIGLU}
+LINEAR_ACTS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU}
 GATES = {"topk": GATE_TOPK, "all": GATE_ALL}
 
 lib_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_wq.so")
@@ -61,6 +67,9 @@ EXPORTED_SYMBOLS = (
     "moe_decode_layer", "moe_decode_workspace_size", "moe_route_topk_active",
     "moe_decode_layer_noalloc", "moe_decode_layer_shared", "moe_decode_shared_workspace_size",
     "moe_elb_accumulate", "moe_elb_top_m", "moe_bf16_recombine",
+    "moe_linear", "moe_linear_workspace_size", "moe_linear_backward",
+    "moe_linear_backward_workspace_size", "moe_balance_loss", "moe_balance_workspace_size",
+    "moe_route_backward", "moe_combine_backward",
 )
 
 
@@ -84,6 +93,8 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _SZ = ctypes.c_size_t
+_L = ctypes.c_int64
+_F = ctypes.c_float
 
 
 def lib():
@@ -134,6 +145,18 @@ def lib():
         "moe_decode_layer_shared": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P,
                                          _I, _I, _P, _P, _I, _P, _P, _P, _P, _SZ, _P]),
         "moe_decode_shared_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+        "moe_linear": (_I, [_P, _L, _P, _L, _P, _P, _L, _I, _I, _I, _I, _I, _P, _L, _I, _P, _L, _P,
+                            _SZ, _P]),
+        "moe_linear_workspace_size": (_SZ, [_I, _I, _I, _L, _L]),
+        "moe_linear_backward": (_I, [_P, _L, _I, _P, _L, _P, _L, _P, _L, _I, _I, _I, _I, _I, _P,
+                                     _P, _P, _P, _SZ, _P]),
+        "moe_linear_backward_workspace_size": (_SZ, [_I, _I, _I, _L, _L, _L, _I, _I]),
+        "moe_balance_loss": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P, _SZ,
+                                  _P]),
+        "moe_balance_workspace_size": (_SZ, [_I, _I, _I]),
+        "moe_route_backward": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _F, _P,
+                                    _P, _P]),
+        "moe_combine_backward": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -559,6 +582,290 @@ def moe_dequant(w_packed, scales, wtype, group_size, E, K, N, out=None, stream=N
     _check("moe_dequant", lib().moe_dequant(_ptr(w_packed), _ptr(scales), WTYPES.get(wtype, wtype),
                                             int(group_size), E, K, N, _ptr(out), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- dense products, router gradients
+_HERE = contextlib.nullcontext()
+
+
+def _place(ref, stream):
+    """The context in which a call on ref's device is made and its outputs and workspace are
+    allocated: that device current, and `stream` (default: the device's current one) its current
+    stream, so that the allocator orders the memory by the stream that uses it."""
+    torch = _torch()
+    dev = ref.device
+    if not ref.is_cuda:
+        raise TypeError("expected device tensors")
+    if stream is None:
+        return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _dense(t, dtype, name, shape, dev):
+    """A dense device tensor of exactly this type, shape and device."""
+    if t is None:
+        return
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, dtype, name, shape, dev):
+    """Row stride of a device matrix of this type and shape whose rows are contiguous (0: None)."""
+    if t is None:
+        return 0
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    rows, cols = shape
+    if rows <= 1 or cols == 0:
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: rows must be contiguous")
+        return cols
+    if (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+    return t.stride(0)
+
+
+def _dt(dtype, name):
+    torch = _torch()
+    if dtype == torch.float16:
+        return DT_FP16
+    if dtype == torch.bfloat16:
+        return DT_BF16
+    raise TypeError(f"{name}: expected torch.float16 or torch.bfloat16, got {dtype}")
+
+
+def _linear_act(act):
+    if act in LINEAR_ACTS:
+        return LINEAR_ACTS[act]
+    if act in LINEAR_ACTS.values():
+        return act
+    raise ValueError(f"act: expected one of {sorted(LINEAR_ACTS)}, got {act!r}")
+
+
+def _workspace(need, ws, dev):
+    torch = _torch()
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _need(ws, torch.uint8, "ws")
+    if ws.device != dev:
+        raise ValueError(f"ws: expected a tensor on {dev}, got {ws.device}")
+    return ws
+
+
+def moe_linear_workspace_size(M, N, K, lda=None, ldw=None):
+    """Workspace bytes of moe_linear; row strides default to dense rows."""
+    return lib().moe_linear_workspace_size(M, N, K, K if lda is None else lda,
+                                           K if ldw is None else ldw)
+
+
+def moe_linear(a, w, bias=None, act="none", residual=None, out=None, out_dtype=None, preact=None,
+               ws=None, stream=None):
+    """act(a @ w.T + bias) + residual for fp16 or bf16 a [M, K] and w [N, K] (rows may be strided).
+    act: "none" | "relu" | "silu" | "gelu".  out_dtype: a's type (default) or torch.float32.
+    preact ([M, N] of a's type): receives the activation's argument for moe_linear_backward.
+    out may be `residual` itself."""
+    torch = _torch()
+    if a.dim() != 2 or w.dim() != 2:
+        raise ValueError("a and w must have two dimensions")
+    M, K = a.shape
+    N = w.shape[0]
+    dev, dtype = a.device, a.dtype
+    dt = _dt(dtype, "a")
+    with _place(a, stream):
+        if out is None:
+            out = new_output((M, N), out_dtype or dtype, dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
+        od = DT_FP32 if out.dtype == torch.float32 else _dt(out.dtype, "out")
+        lda = _rows(a, dtype, "a", (M, K), dev)
+        ldw = _rows(w, dtype, "w", (N, K), dev)
+        ldr = _rows(residual, dtype, "residual", (M, N), dev)
+        ldo = _rows(out, out.dtype, "out", (M, N), dev)
+        ldp = _rows(preact, dtype, "preact", (M, N), dev)
+        _dense(bias, dtype, "bias", (N,), dev)
+        ac = _linear_act(act)
+        L = lib()
+        ws = _workspace(L.moe_linear_workspace_size(M, N, K, lda, ldw), ws, dev)
+        _check("moe_linear", L.moe_linear(
+            _at(a), lda, _at(w), ldw, _at(bias), _at(residual), ldr, M, N, K, dt, ac, _at(out),
+            ldo, od, _at(preact), ldp, _at(ws), 0 if ws is None else ws.numel(), _stream(None)))
+    return out
+
+
+def moe_linear_backward_workspace_size(M, N, K, lda=None, ldw=None, ldg=None, grad_f32=False,
+                                       act="none"):
+    """Workspace bytes of moe_linear_backward; row strides default to dense rows."""
+    return lib().moe_linear_backward_workspace_size(
+        M, N, K, K if lda is None else lda, K if ldw is None else ldw, N if ldg is None else ldg,
+        DT_FP32 if grad_f32 else DT_FP16, _linear_act(act))
+
+
+def moe_linear_backward(grad_out, a, w, act="none", preact=None, need_a=True, need_w=True,
+                        need_bias=True, grad_a=None, grad_w=None, grad_bias=None, ws=None,
+                        stream=None):
+    """Gradients (grad_a [M, K], grad_w [N, K], grad_bias [N], of a's type; None where not needed)
+    of moe_linear.  grad_out [M, N] of a's type or float32; preact: what moe_linear stored."""
+    torch = _torch()
+    if a.dim() != 2 or w.dim() != 2:
+        raise ValueError("a and w must have two dimensions")
+    M, K = a.shape
+    N = w.shape[0]
+    dev, dtype = a.device, a.dtype
+    dt = _dt(dtype, "a")
+    ac = _linear_act(act)
+    with _place(a, stream):
+        if grad_a is None and need_a:
+            grad_a = new_output((M, K), dtype, dev)
+        if grad_w is None and need_w:
+            grad_w = new_output((N, K), dtype, dev)
+        if grad_bias is None and need_bias:
+            grad_bias = new_output((N,), dtype, dev)
+        gd = grad_out.dtype
+        gdt = DT_FP32 if gd == torch.float32 else _dt(gd, "grad_out")
+        ldg = _rows(grad_out, gd, "grad_out", (M, N), dev)
+        lda = _rows(a, dtype, "a", (M, K), dev)
+        ldw = _rows(w, dtype, "w", (N, K), dev)
+        ldp = _rows(preact, dtype, "preact", (M, N), dev)
+        _dense(grad_a, dtype, "grad_a", (M, K), dev)
+        _dense(grad_w, dtype, "grad_w", (N, K), dev)
+        _dense(grad_bias, dtype, "grad_bias", (N,), dev)
+        L = lib()
+        ws = _workspace(L.moe_linear_backward_workspace_size(M, N, K, lda, ldw, ldg, gdt, ac), ws,
+                        dev)
+        _check("moe_linear_backward", L.moe_linear_backward(
+            _at(grad_out), ldg, gdt, _at(preact), ldp, _at(a), lda, _at(w), ldw, M, N, K, dt, ac,
+            _at(grad_a), _at(grad_w), _at(grad_bias), _at(ws), 0 if ws is None else ws.numel(),
+            _stream(None)))
+    return grad_a, grad_w, grad_bias
+
+
+def moe_balance_workspace_size(T, E, S=1):
+    return lib().moe_balance_workspace_size(T, E, S)
+
+
+def _segments(seq_offsets, dev):
+    """Number of segments of seq_offsets (int32 [S + 1], or None: one)."""
+    if seq_offsets is None:
+        return 1
+    S = seq_offsets.numel() - 1
+    _dense(seq_offsets, _torch().int32, "seq_offsets", (S + 1,), dev)
+    if S < 1:
+        raise ValueError("seq_offsets needs at least two entries")
+    return S
+
+
+def moe_balance_loss(logits, topk_ids, coef, active=None, seq_offsets=None, loss=None, counts=None,
+                     probs=None, tokens=None, ws=None, stream=None):
+    """Router balance loss of fp32 logits [T, E] and routed ids [T, k]: returns (loss fp32 [1],
+    counts int32 [S, E], probs fp32 [S, E], tokens int32 [S]); S = 1 without seq_offsets."""
+    torch = _torch()
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    dev = logits.device
+    with _place(logits, stream):
+        S = _segments(seq_offsets, dev)
+        if loss is None:
+            loss = new_output((1,), torch.float32, dev)
+        if counts is None:
+            counts = new_output((S, E), torch.int32, dev)
+        if probs is None:
+            probs = new_output((S, E), torch.float32, dev)
+        if tokens is None:
+            tokens = new_output((S,), torch.int32, dev)
+        _dense(logits, torch.float32, "logits", (T, E), dev)
+        _dense(topk_ids, torch.int32, "topk_ids", (T, k), dev)
+        _dense(active, torch.uint8, "active", (T,), dev)
+        _dense(loss, torch.float32, "loss", (1,), dev)
+        _dense(counts, torch.int32, "counts", (S, E), dev)
+        _dense(probs, torch.float32, "probs", (S, E), dev)
+        _dense(tokens, torch.int32, "tokens", (S,), dev)
+        L = lib()
+        ws = _workspace(L.moe_balance_workspace_size(T, E, S), ws, dev)
+        _check("moe_balance_loss", L.moe_balance_loss(
+            _at(logits), _at(topk_ids), _at(active), _at(seq_offsets), S, T, E, k, float(coef),
+            _at(loss), _at(counts), _at(probs), _at(tokens), _at(ws),
+            0 if ws is None else ws.numel(), _stream(None)))
+    return loss, counts, probs, tokens
+
+
+def moe_route_backward(logits, topk_ids, gate_mode="topk", topk_w=None, grad_w=None, active=None,
+                       counts=None, tokens=None, coef=0.0, grad_loss=None, seq_offsets=None,
+                       grad_logits=None, stream=None):
+    """Gradient fp32 [T, E] of the router logits through the gate weights (topk_w with their
+    gradient grad_w, both fp32 [T, k]), the balance loss (counts and tokens of moe_balance_loss,
+    its coef and seq_offsets, grad_loss fp32 [1] or None for 1), or both."""
+    torch = _torch()
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    dev = logits.device
+    with _place(logits, stream):
+        S = _segments(seq_offsets, dev)
+        if grad_logits is None:
+            grad_logits = new_output((T, E), torch.float32, dev)
+        _dense(logits, torch.float32, "logits", (T, E), dev)
+        _dense(topk_ids, torch.int32, "topk_ids", (T, k), dev)
+        _dense(topk_w, torch.float32, "topk_w", (T, k), dev)
+        _dense(grad_w, torch.float32, "grad_w", (T, k), dev)
+        _dense(active, torch.uint8, "active", (T,), dev)
+        _dense(counts, torch.int32, "counts", (S, E), dev)
+        _dense(tokens, torch.int32, "tokens", (S,), dev)
+        _dense(grad_loss, torch.float32, "grad_loss", (1,), dev)
+        _dense(grad_logits, torch.float32, "grad_logits", (T, E), dev)
+        _check("moe_route_backward", lib().moe_route_backward(
+            _at(logits), _at(topk_ids), _at(topk_w), _at(grad_w), _at(active), _at(seq_offsets), S,
+            T, E, k, GATES.get(gate_mode, gate_mode), _at(counts), _at(tokens), float(coef),
+            _at(grad_loss), _at(grad_logits), _stream(None)))
+    return grad_logits
+
+
+def moe_combine_backward(grad_out, y_perm, inv_perm, topk_w, need_w=True, need_y=True, grad_w=None,
+                         grad_y=None, stream=None):
+    """Gradients (grad_w fp32 [T, k], grad_y fp16 like y_perm; None where not needed) of
+    moe_unpermute_combine called with topk_w [T, k] on unscaled expert rows y_perm [R, d]."""
+    torch = _torch()
+    T, d = grad_out.shape
+    k = topk_w.shape[1]
+    R = y_perm.shape[0]
+    dev = grad_out.device
+    with _place(grad_out, stream):
+        if grad_w is None and need_w:
+            grad_w = new_output((T, k), torch.float32, dev)
+        if grad_y is None and need_y:
+            grad_y = new_output((R, d), torch.float16, dev)
+        _dense(grad_out, torch.float16, "grad_out", (T, d), dev)
+        _dense(y_perm, torch.float16, "y_perm", (R, d), dev)
+        if R < T * k:
+            raise ValueError(f"y_perm: needs at least {T * k} rows, has {R}")
+        _dense(inv_perm, torch.int32, "inv_perm", (T * k,), dev)
+        _dense(topk_w, torch.float32, "topk_w", (T, k), dev)
+        _dense(grad_w, torch.float32, "grad_w", (T, k), dev)
+        _dense(grad_y, torch.float16, "grad_y", (R, d), dev)
+        _check("moe_combine_backward", lib().moe_combine_backward(
+            _at(grad_out), _at(y_perm), _at(inv_perm), _at(topk_w), T, k, d, _at(grad_w),
+            _at(grad_y), _stream(None)))
+    return grad_w, grad_y
 
 
 # ---------------------------------------------------------------- host helpers

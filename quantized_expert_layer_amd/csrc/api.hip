@@ -480,6 +480,384 @@ int32_t moe_bf16_recombine(const uint8_t* exponents, const uint8_t* sign_mantiss
                                                  (hipStream_t)stream));
 }
 
+// ---- balance loss and the router's gradients ----
+static int32_t validate_segments(int32_t S, int32_t T, int32_t E, int32_t k,
+                                 const int32_t* seq_offsets) {
+    if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || k < 1 || k > MOE_MAX_TOPK || S < 1)
+        return MOE_ERR_INVALID;
+    if (!seq_offsets && S != 1) return MOE_ERR_INVALID;
+    if (!aligned(seq_offsets, 4)) return MOE_ERR_INVALID;
+    if (T >= 1 << 28 || S > 1 << 20 || (int64_t)T * E >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+size_t moe_balance_workspace_size(int32_t T, int32_t E, int32_t S) {
+    static const int32_t any = 0;
+    if (validate_segments(S, T, E, 1, &any) != MOE_OK) return 0;
+    return moe::balance_workspace_layout(T, E, S, nullptr, nullptr);
+}
+
+int32_t moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* active,
+                         const int32_t* seq_offsets, int32_t S, int32_t T, int32_t E, int32_t k,
+                         float coef, float* loss, int32_t* counts, float* probs, int32_t* tokens,
+                         void* ws, size_t ws_bytes, void* stream) {
+    if (int32_t st = validate_segments(S, T, E, k, seq_offsets)) return st;
+    if (!loss || !counts || !probs || !tokens || (T > 0 && (!logits || !topk_ids)))
+        return MOE_ERR_INVALID;
+    if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(loss, 4) || !aligned(counts, 4) ||
+        !aligned(probs, 4) || !aligned(tokens, 4))
+        return MOE_ERR_INVALID;
+    const size_t need = moe::balance_workspace_layout(T, E, S, nullptr, nullptr);
+    if (!ws || ws_bytes < need || !aligned(ws, 16)) return MOE_ERR_WORKSPACE;
+    if (int32_t st = check_device()) return st;
+    moe::BalanceParams p;
+    p.logits = logits;
+    p.ids = topk_ids;
+    p.active = active;
+    p.offsets = seq_offsets;
+    p.S = S;
+    p.T = T;
+    p.E = E;
+    p.k = k;
+    p.coef = coef;
+    p.loss = loss;
+    p.counts = counts;
+    p.probs = probs;
+    p.tokens = tokens;
+    moe::balance_workspace_layout(T, E, S, &p, (char*)ws);
+    return hip_status(moe::launch_balance(p, (hipStream_t)stream));
+}
+
+int32_t moe_route_backward(const float* logits, const int32_t* topk_ids, const float* topk_w,
+                           const float* grad_w, const uint8_t* active, const int32_t* seq_offsets,
+                           int32_t S, int32_t T, int32_t E, int32_t k, int32_t gate_mode,
+                           const int32_t* counts, const int32_t* tokens, float coef,
+                           const float* grad_loss, float* grad_logits, void* stream) {
+    if (int32_t st = validate_segments(S, T, E, k, seq_offsets)) return st;
+    if (gate_mode != MOE_GATE_SOFTMAX_TOPK && gate_mode != MOE_GATE_SOFTMAX_ALL)
+        return MOE_ERR_INVALID;
+    if (!grad_w && !counts) return MOE_ERR_INVALID;
+    if ((counts != nullptr) != (tokens != nullptr)) return MOE_ERR_INVALID;
+    if (T == 0) return MOE_OK;
+    if (!logits || !grad_logits || (grad_w && (!topk_ids || !topk_w))) return MOE_ERR_INVALID;
+    if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(grad_w, 4) ||
+        !aligned(counts, 4) || !aligned(tokens, 4) || !aligned(grad_loss, 4) ||
+        !aligned(grad_logits, 4))
+        return MOE_ERR_INVALID;
+    if (int32_t st = check_device()) return st;
+    moe::RouteGradParams p;
+    p.logits = logits;
+    p.ids = topk_ids;
+    p.topk_w = topk_w;
+    p.grad_w = grad_w;
+    p.active = active;
+    p.offsets = seq_offsets;
+    p.S = S;
+    p.T = T;
+    p.E = E;
+    p.k = k;
+    p.gate_all = gate_mode == MOE_GATE_SOFTMAX_ALL;
+    p.counts = counts;
+    p.tokens = tokens;
+    p.coef = coef;
+    p.grad_loss = grad_loss;
+    p.grad = grad_logits;
+    return hip_status(moe::launch_route_backward(p, (hipStream_t)stream));
+}
+
+int32_t moe_combine_backward(const uint16_t* grad_out, const uint16_t* y_perm,
+                             const int32_t* inv_perm, const float* topk_w, int32_t T, int32_t k,
+                             int32_t d, float* grad_w, uint16_t* grad_y, void* stream) {
+    if (T < 0 || k < 1 || k > MOE_MAX_TOPK || d <= 0) return MOE_ERR_INVALID;
+    if (!grad_w && !grad_y) return MOE_ERR_INVALID;
+    if (d % 8 != 0 || T >= 1 << 24) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!grad_out || !inv_perm || (grad_w && !y_perm) || (grad_y && !topk_w)) return MOE_ERR_INVALID;
+    if (!aligned(grad_out, 16) || !aligned(y_perm, 16) || !aligned(inv_perm, 4) ||
+        !aligned(topk_w, 4) || !aligned(grad_w, 4) || !aligned(grad_y, 16))
+        return MOE_ERR_INVALID;
+    if (int32_t st = check_device()) return st;
+    moe::CombineGradParams p;
+    p.grad_out = grad_out;
+    p.y = y_perm;
+    p.inv_perm = inv_perm;
+    p.topk_w = topk_w;
+    p.T = T;
+    p.k = k;
+    p.d = d;
+    p.grad_w = grad_w;
+    p.grad_y = grad_y;
+    return hip_status(moe::launch_combine_backward(p, (hipStream_t)stream));
+}
+
+// ---- dense linear layer and its gradients ----
+namespace {
+
+constexpr int64_t kLinearMaxStride = (int64_t)1 << 22;   // a tile's byte offsets stay below 2^31
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+int up8(int n) { return (n + 7) / 8 * 8; }
+
+// Rows that 16-byte pieces can read in place.
+bool in_pieces(int cols, int64_t ld) { return cols % 8 == 0 && ld % 8 == 0; }
+
+int32_t validate_linear_sizes(int32_t M, int32_t N, int32_t K, int32_t dtype, int32_t act) {
+    if (M < 0 || N < 0 || K < 1) return MOE_ERR_INVALID;
+    if (dtype != MOE_DT_FP16 && dtype != MOE_DT_BF16) return MOE_ERR_INVALID;
+    if (act < MOE_ACT_NONE || act > MOE_ACT_GELU) return MOE_ERR_INVALID;
+    if (act == MOE_ACT_SWIGLU) return MOE_ERR_UNSUPPORTED;
+    if (K > kLinearMaxStride || N > kLinearMaxStride || M > 1 << 28) return MOE_ERR_UNSUPPORTED;
+    if ((int64_t)M * N >= (int64_t)1 << 36 || (int64_t)M * K >= (int64_t)1 << 36 ||
+        (int64_t)N * K >= (int64_t)1 << 36)
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+int32_t validate_stride(int64_t ld, int32_t cols) {
+    if (ld < cols) return MOE_ERR_INVALID;
+    return ld > kLinearMaxStride ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+// Hands out 256-byte aligned pieces of a workspace (base NULL: only counts).
+struct Carver {
+    char* base;
+    size_t used = 0;
+    void* take(size_t bytes) {
+        void* p = base ? base + used : nullptr;
+        used += up256(bytes);
+        return p;
+    }
+};
+
+struct LinearForward {
+    moe::LinearProduct p;
+    uint16_t *pack_a, *pack_w;
+};
+
+// Sizes and workspace of moe_linear (pointers are filled in by the caller).
+LinearForward linear_forward(int32_t M, int32_t N, int32_t K, int64_t lda, int64_t ldw, Carver& c) {
+    LinearForward f{};
+    moe::LinearProduct& p = f.p;
+    p.lda = lda;
+    p.ldb = ldw;
+    p.M = p.a_outs = M;
+    p.N = p.b_outs = N;
+    p.red = p.b_red = up8(K);
+    p.parts = 1;
+    if (!in_pieces(K, lda)) {
+        f.pack_a = (uint16_t*)c.take((size_t)M * up8(K) * 2);
+        p.lda = up8(K);
+    }
+    if (!in_pieces(K, ldw)) {
+        f.pack_w = (uint16_t*)c.take((size_t)N * up8(K) * 2);
+        p.ldb = up8(K);
+    }
+    moe::linear_plan(p);
+    if (p.split > 1) p.part = (float*)c.take(moe::linear_part_bytes(p));
+    return f;
+}
+
+struct LinearBackward {
+    moe::LinearProduct da, dw;
+    moe::LinearDz dz;
+    uint16_t *pack_a, *pack_w;
+    bool need_dz;             // the products read a copy of the gradient
+};
+
+LinearBackward linear_backward(int32_t M, int32_t N, int32_t K, int64_t lda, int64_t ldw, int64_t ldg,
+                               int32_t grad_dtype, int32_t act, Carver& c) {
+    LinearBackward f{};
+    const int N8 = up8(N), K8 = up8(K);
+    f.need_dz = grad_dtype == MOE_DT_FP32 || act != MOE_ACT_NONE || !in_pieces(N, ldg);
+    const int parts = grad_dtype == MOE_DT_FP32 ? 2 : 1;
+    f.dz.cols8 = N8;
+    f.dz.parts = parts;
+    const int64_t ldz = f.need_dz ? N8 : ldg;
+    if (f.need_dz) f.dz.dz = (uint16_t*)c.take((size_t)parts * M * N8 * 2);
+    f.dz.sums = (float*)c.take((size_t)moe::linear_dz_blocks(M) * N * 4);
+    if (!in_pieces(K, ldw)) {
+        f.pack_w = (uint16_t*)c.take((size_t)N * K8 * 2);
+        ldw = K8;
+    }
+    if (!in_pieces(K, lda)) {
+        f.pack_a = (uint16_t*)c.take((size_t)M * K8 * 2);
+        lda = K8;
+    }
+    // da[m, k] = sum_n dz[m][n] w[n][k]
+    f.da.lda = ldz;
+    f.da.ldb = ldw;
+    f.da.b_cols = 1;
+    f.da.M = f.da.a_outs = M;
+    f.da.N = K;
+    f.da.b_outs = K8;
+    f.da.red = N8;
+    f.da.b_red = N;
+    f.da.parts = parts;
+    f.da.a_part = (int64_t)M * N8;
+    moe::linear_plan(f.da);
+    // dw[n, k] = sum_m dz[m][n] a[m][k]
+    f.dw.lda = ldz;
+    f.dw.ldb = lda;
+    f.dw.a_cols = f.dw.b_cols = 1;
+    f.dw.M = N;
+    f.dw.a_outs = N8;
+    f.dw.N = K;
+    f.dw.b_outs = K8;
+    f.dw.red = f.dw.b_red = M;
+    f.dw.parts = parts;
+    f.dw.a_part = (int64_t)M * N8;
+    moe::linear_plan(f.dw);
+    const size_t pa = moe::linear_part_bytes(f.da), pw = moe::linear_part_bytes(f.dw);
+    float* part = (float*)c.take(pa > pw ? pa : pw);       // the products run one after the other
+    f.da.part = f.da.split > 1 ? part : nullptr;
+    f.dw.part = f.dw.split > 1 ? part : nullptr;
+    return f;
+}
+
+void grad_out_epilogue(moe::LinearEpilogue& e, uint16_t* out, int32_t K) {
+    e.out = out;
+    e.ldo = K;
+    e.vec_out = K % 4 == 0;
+}
+
+}  // namespace
+
+size_t moe_linear_workspace_size(int32_t M, int32_t N, int32_t K, int64_t lda, int64_t ldw) {
+    if (validate_linear_sizes(M, N, K, MOE_DT_FP16, MOE_ACT_NONE) != MOE_OK || M == 0 || N == 0)
+        return 0;
+    Carver c{nullptr};
+    linear_forward(M, N, K, lda, ldw, c);
+    return c.used;
+}
+
+int32_t moe_linear(const uint16_t* a, int64_t lda, const uint16_t* w, int64_t ldw,
+                   const uint16_t* bias, const uint16_t* residual, int64_t ldr, int32_t M,
+                   int32_t N, int32_t K, int32_t dtype, int32_t act, void* out, int64_t ldo,
+                   int32_t out_dtype, uint16_t* preact, int64_t ldp, void* ws, size_t ws_bytes,
+                   void* stream) {
+    if (int32_t st = validate_linear_sizes(M, N, K, dtype, act)) return st;
+    if (out_dtype < MOE_DT_FP16 || out_dtype > MOE_DT_FP32) return MOE_ERR_INVALID;
+    if (out_dtype != dtype && out_dtype != MOE_DT_FP32) return MOE_ERR_UNSUPPORTED;
+    if (int32_t st = validate_stride(lda, K)) return st;
+    if (int32_t st = validate_stride(ldw, K)) return st;
+    if (int32_t st = validate_stride(ldo, N)) return st;
+    if (residual)
+        if (int32_t st = validate_stride(ldr, N)) return st;
+    if (preact)
+        if (int32_t st = validate_stride(ldp, N)) return st;
+    if (M == 0 || N == 0) return MOE_OK;
+    if (!a || !w || !out) return MOE_ERR_INVALID;
+    if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(residual, 16) ||
+        !aligned(preact, 16) || !aligned(bias, 2))
+        return MOE_ERR_INVALID;
+    if (preact && (void*)preact == out) return MOE_ERR_INVALID;
+    if (residual && (const void*)residual == out && (ldr != ldo || out_dtype != dtype))
+        return MOE_ERR_INVALID;
+    Carver c{(char*)ws};
+    LinearForward f = linear_forward(M, N, K, lda, ldw, c);
+    if (c.used && (!ws || ws_bytes < c.used || !aligned(ws, 16))) return MOE_ERR_WORKSPACE;
+    if (int32_t st = check_device()) return st;
+    hipStream_t s = (hipStream_t)stream;
+    moe::LinearProduct& p = f.p;
+    p.a = a;
+    p.b = w;
+    if (f.pack_a) {
+        if (moe::launch_linear_pack(a, lda, M, K, f.pack_a, s) != hipSuccess) return MOE_ERR_HIP;
+        p.a = f.pack_a;
+    }
+    if (f.pack_w) {
+        if (moe::launch_linear_pack(w, ldw, N, K, f.pack_w, s) != hipSuccess) return MOE_ERR_HIP;
+        p.b = f.pack_w;
+    }
+    moe::LinearEpilogue& e = p.epi;
+    e.bias = bias;
+    e.residual = residual;
+    e.ldr = ldr;
+    e.preact = preact;
+    e.ldp = ldp;
+    e.out = out;
+    e.ldo = ldo;
+    e.out_f32 = out_dtype == MOE_DT_FP32;
+    e.act = act;
+    e.vec_out = ldo % 4 == 0;
+    e.vec_res = ldr % 4 == 0;
+    e.vec_pre = ldp % 4 == 0;
+    return hip_status(moe::launch_linear_product(p, dtype, s));
+}
+
+size_t moe_linear_backward_workspace_size(int32_t M, int32_t N, int32_t K, int64_t lda, int64_t ldw,
+                                          int64_t ldg, int32_t grad_dtype, int32_t act) {
+    if (validate_linear_sizes(M, N, K, MOE_DT_FP16, act) != MOE_OK) return 0;
+    Carver c{nullptr};
+    linear_backward(M, N, K, lda, ldw, ldg, grad_dtype, act, c);
+    return c.used;
+}
+
+int32_t moe_linear_backward(const void* grad_out, int64_t ldg, int32_t grad_dtype,
+                            const uint16_t* preact, int64_t ldp, const uint16_t* a, int64_t lda,
+                            const uint16_t* w, int64_t ldw, int32_t M, int32_t N, int32_t K,
+                            int32_t dtype, int32_t act, uint16_t* grad_a, uint16_t* grad_w,
+                            uint16_t* grad_bias, void* ws, size_t ws_bytes, void* stream) {
+    if (int32_t st = validate_linear_sizes(M, N, K, dtype, act)) return st;
+    if (grad_dtype < MOE_DT_FP16 || grad_dtype > MOE_DT_FP32) return MOE_ERR_INVALID;
+    if (grad_dtype != dtype && grad_dtype != MOE_DT_FP32) return MOE_ERR_UNSUPPORTED;
+    if (!grad_a && !grad_w && !grad_bias) return MOE_ERR_INVALID;
+    if (int32_t st = validate_stride(ldg, N)) return st;
+    if (act != MOE_ACT_NONE)
+        if (int32_t st = validate_stride(ldp, N)) return st;
+    if (int32_t st = validate_stride(lda, K)) return st;
+    if (int32_t st = validate_stride(ldw, K)) return st;
+    if (M > 0 && N > 0) {
+        if (!grad_out || (act != MOE_ACT_NONE && !preact)) return MOE_ERR_INVALID;
+        if ((grad_a && !w) || (grad_w && !a)) return MOE_ERR_INVALID;
+    }
+    if (!aligned(grad_out, 16) || !aligned(preact, 16) || !aligned(a, 16) || !aligned(w, 16) ||
+        !aligned(grad_a, 16) || !aligned(grad_w, 16) || !aligned(grad_bias, 2))
+        return MOE_ERR_INVALID;
+    if ((M == 0 || !grad_a) && (N == 0 || (!grad_w && !grad_bias))) return MOE_OK;
+    Carver c{(char*)ws};
+    LinearBackward f = linear_backward(M, N, K, lda, ldw, ldg, grad_dtype, act, c);
+    if (c.used && (!ws || ws_bytes < c.used || !aligned(ws, 16))) return MOE_ERR_WORKSPACE;
+    if (int32_t st = check_device()) return st;
+    hipStream_t s = (hipStream_t)stream;
+    if (N > 0 && (f.need_dz || grad_bias)) {
+        moe::LinearDz& z = f.dz;
+        z.grad = grad_out;
+        z.ldg = ldg;
+        z.grad_f32 = grad_dtype == MOE_DT_FP32;
+        z.preact = preact;
+        z.ldp = ldp;
+        z.act = act;
+        z.M = M;
+        z.N = N;
+        if (!grad_a && !grad_w) z.dz = nullptr;
+        if (!grad_bias) z.sums = nullptr;
+        if (moe::launch_linear_dz(z, dtype, grad_bias, s) != hipSuccess) return MOE_ERR_HIP;
+    }
+    const uint16_t* dz = f.need_dz ? f.dz.dz : (const uint16_t*)grad_out;
+    if (grad_a && M > 0) {
+        f.da.a = dz;
+        f.da.b = w;
+        if (f.pack_w) {
+            if (moe::launch_linear_pack(w, ldw, N, K, f.pack_w, s) != hipSuccess) return MOE_ERR_HIP;
+            f.da.b = f.pack_w;
+        }
+        grad_out_epilogue(f.da.epi, grad_a, K);
+        if (moe::launch_linear_product(f.da, dtype, s) != hipSuccess) return MOE_ERR_HIP;
+    }
+    if (grad_w && N > 0) {
+        f.dw.a = dz;
+        f.dw.b = a;
+        if (f.pack_a) {
+            if (moe::launch_linear_pack(a, lda, M, K, f.pack_a, s) != hipSuccess) return MOE_ERR_HIP;
+            f.dw.b = f.pack_a;
+        }
+        grad_out_epilogue(f.dw.epi, grad_w, K);
+        if (moe::launch_linear_product(f.dw, dtype, s) != hipSuccess) return MOE_ERR_HIP;
+    }
+    return MOE_OK;
+}
+
 int32_t moe_dequant(const void* w_packed, const uint16_t* scales, int32_t wtype, int32_t group_size,
                     int32_t E, int32_t K, int32_t N, uint16_t* w_out, void* stream) {
     if (E < 1 || E > MOE_MAX_EXPERTS || K <= 0 || N <= 0) return MOE_ERR_INVALID;

@@ -129,4 +129,103 @@ size_t decode_workspace_layout(int T, int k, int E, int d, int inter, int wtype,
                                DecodeWs* ws, char* base);
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream);
 
+// ---- dense linear layer and its gradients ----
+constexpr int kLinearMaxSplit = 16;
+
+struct LinearEpilogue {      // out = act(sum + bias) + residual; preact = sum + bias
+    const uint16_t* bias;    // [N] or NULL
+    const uint16_t* residual;
+    int64_t ldr;
+    uint16_t* preact;        // [M, N] or NULL
+    int64_t ldp;
+    void* out;               // 16-bit of the operands' type, or fp32
+    int64_t ldo;
+    int out_f32, act;
+    int vec_out, vec_res, vec_pre;   // four columns of a row are one aligned access
+};
+
+struct LinearProduct {       // C[i, j] = sum over parts and r < red of A[i, r] B[j, r]
+    const uint16_t* a;
+    const uint16_t* b;
+    int64_t lda, ldb;
+    int64_t a_part, b_part;  // elements from one part of the summed index to the next
+    int a_cols, b_cols;      // operand stored with its output index contiguous
+    int a_outs, b_outs;      // output indices the operands hold (>= M, N: padded copies)
+    int red, b_red, parts;   // summed indices per part (b_red: rows B really has); 1 or 2 parts
+    int M, N;
+    LinearEpilogue epi;
+    float* part;             // fp32 [split, M, ldpart] when split > 1
+    int ldpart, split, cfg, tiles_m, tiles_n;
+};
+
+struct LinearDz {
+    const void* grad;        // [M, N], 16-bit or fp32
+    int64_t ldg;
+    int grad_f32;
+    const uint16_t* preact;
+    int64_t ldp;
+    int act, M, N, cols8;
+    uint16_t* dz;            // [parts, M, cols8] or NULL
+    int parts;
+    float* sums;             // [linear_dz_blocks(M), N] or NULL
+};
+
+// Chooses tile, split and the partial layout from the sizes (host-only, deterministic).
+void linear_plan(LinearProduct& p);
+size_t linear_part_bytes(const LinearProduct& p);
+hipError_t launch_linear_product(const LinearProduct& p, int dtype, hipStream_t stream);
+hipError_t launch_linear_pack(const uint16_t* src, int64_t ld, int rows, int cols, uint16_t* dst,
+                              hipStream_t stream);
+int linear_dz_blocks(int M);
+hipError_t launch_linear_dz(const LinearDz& p, int dtype, uint16_t* grad_bias, hipStream_t stream);
+
+// ---- balance loss and the router's gradients ----
+struct BalanceParams {
+    const float* logits;     // [T, E]
+    const int32_t* ids;      // [T, k]
+    const uint8_t* active;   // [T] or NULL
+    const int32_t* offsets;  // [S + 1] or NULL (S == 1: all tokens)
+    int S, T, E, k;
+    float coef;
+    float* loss;
+    int32_t* counts;
+    float* probs;
+    int32_t* tokens;
+    int cell, pieces;        // tokens per cell; pieces of the batch (blocks)
+    int* arrived;            // workspace: segments done
+    float* part_sums;        // [pieces, E] probability sums
+    int32_t* part_counts;    // [pieces, E]
+    int32_t* part_tokens;    // [pieces]
+    float* terms;            // [S]
+};
+size_t balance_workspace_layout(int T, int E, int S, BalanceParams* p, char* base);
+hipError_t launch_balance(const BalanceParams& p, hipStream_t stream);
+
+struct RouteGradParams {
+    const float* logits;
+    const int32_t* ids;
+    const float* topk_w;
+    const float* grad_w;     // or NULL: no gate term
+    const uint8_t* active;
+    const int32_t* offsets;
+    int S, T, E, k, gate_all;
+    const int32_t* counts;   // or NULL: no balance term
+    const int32_t* tokens;
+    float coef;
+    const float* grad_loss;  // or NULL: 1
+    float* grad;
+};
+hipError_t launch_route_backward(const RouteGradParams& p, hipStream_t stream);
+
+struct CombineGradParams {
+    const uint16_t* grad_out;
+    const uint16_t* y;
+    const int32_t* inv_perm;
+    const float* topk_w;
+    int T, k, d;
+    float* grad_w;           // or NULL
+    uint16_t* grad_y;        // or NULL
+};
+hipError_t launch_combine_backward(const CombineGradParams& p, hipStream_t stream);
+
 }  // namespace moe

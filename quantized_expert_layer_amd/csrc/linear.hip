@@ -1,0 +1,268 @@
+// Dense linear layer beside the experts: out = act(a w^T + bias) + residual, and its gradients.
+#include <type_traits>
+
+#include "linear.hpp"
+
+namespace moe {
+
+// ------------------------------------------------------------------------------------
+// Tile product.  A block computes BM x BN outputs with WM x WN waves; a stage (64 summed
+// indices) of both operands is loaded into LDS while the previous one is multiplied.
+// ------------------------------------------------------------------------------------
+template <int DT, bool ACOLS, bool BCOLS, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearProduct p) {
+#ifdef __HIP_DEVICE_COMPILE__                  // the host pass has no buffer resources
+    constexpr int W = WM * WN;
+    constexpr int TM = BM / WM / 16, TN = BN / WN / 16;        // 16x16 subtiles per wave
+    using OA = Operand<BM, ACOLS, W>;
+    using OB = Operand<BN, BCOLS, W>;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * (OA::kBytes + OB::kBytes)];
+
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave / WN, wn = wave % WN;
+
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int z = blockIdx.x / tiles;                          // split of the summed index
+    int tm, tn;
+    tile_of(p, blockIdx.x - z * tiles, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+
+    OA oa;
+    OB ob;
+    oa.init(p.a, p.lda, m0, p.a_outs, p.red, wave, lane);
+    ob.init(p.b, p.ldb, n0, p.b_outs, p.b_red, wave, lane);
+
+    f32x4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // stages [s0, s1) of parts * per_part
+    const int per = (p.red + kBK - 1) / kBK;
+    const int total = per * p.parts;
+    const int s0 = (int)((int64_t)total * z / p.split), s1 = (int)((int64_t)total * (z + 1) / p.split);
+    auto load = [&](int s, int buf) {
+        const int part = s >= per ? 1 : 0;
+        const int k0 = (s - part * per) * kBK;
+        char* dst = lds + buf * (OA::kBytes + OB::kBytes);
+        oa.load(k0, oa.base + part * p.a_part, dst, wave);
+        ob.load(k0, ob.base + part * p.b_part, dst + OA::kBytes, wave);
+    };
+    if (s0 < s1) load(s0, 0);
+    for (int s = s0; s < s1; ++s) {
+        const int buf = (s - s0) & 1;
+        __builtin_amdgcn_s_waitcnt(0x0f70);                    // vmcnt(0): this wave's loads landed
+        __builtin_amdgcn_s_barrier();                          // and everyone's; other buffer free
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + 1 < s1) load(s + 1, buf ^ 1);
+        const char* la = lds + buf * (OA::kBytes + OB::kBytes);
+        const char* lb = la + OA::kBytes;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            s16x8 fa[TM], fb[TN];
+#pragma unroll
+            for (int i = 0; i < TM; ++i) fa[i] = OA::frag(la, (wm * TM + i) * 16, ks, lane);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) fb[j] = OB::frag(lb, (wn * TN + j) * 16, ks, lane);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[i][j] = mfma_dt<DT>(fb[j], fa[i], acc[i][j]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // The accumulators (lane: row lane & 15 of a subtile, columns 4 (lane >> 4) .. + 3) leave
+    // through the wave's own piece of LDS, two subtile rows at a time, so that a row's stores are
+    // whole cache lines and the epilogue's code stands once.
+    constexpr int LPR = TN * 4, RPI = kWave / LPR;             // lanes per row, rows at a time
+    constexpr int RS = TN * 16 + 4;                            // fp32 row stride, padded
+    static_assert(W * 32 * RS * 4 <= (int)sizeof(lds) && TM % 2 == 0, "epilogue staging");
+    __syncthreads();
+    float* region = (float*)lds + wave * 32 * RS;
+    const int lr = lane / LPR, lc = (lane % LPR) * 4;
+    const int col = n0 + wn * TN * 16 + lc;
+#pragma unroll
+    for (int h = 0; h < TM; h += 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                *(f32x4*)(region + (i * 16 + (lane & 15)) * RS + j * 16 + 4 * (lane >> 4)) = acc[h + i][j];
+        lds_wave_fence();
+        const int row0 = m0 + (wm * TM + h) * 16 + lr;
+        for (int r = 0; r < 32; r += RPI) {
+            const int row = row0 + r;
+            if (row < p.M && col < p.N) {
+                const f32x4 v = *(const f32x4*)(region + (r + lr) * RS + lc);
+                if (p.part) *(f32x4*)(p.part + ((int64_t)z * p.M + row) * p.ldpart + col) = v;
+                else linear_epilogue4<DT>(p.epi, v, row, col, p.N);
+            }
+        }
+        lds_wave_fence();
+    }
+#endif
+}
+
+// Sums the splits' partial products in their order and applies the epilogue.
+template <int DT>
+__global__ __launch_bounds__(256) void linear_reduce_kernel(LinearProduct p) {
+    const int n4 = (p.N + 3) / 4;
+    const int64_t total = (int64_t)p.M * n4;
+    for (int64_t i = blockIdx.x * 256 + (int64_t)threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / n4;
+        const int col = (int)(i - row * n4) * 4;
+        const float* src = p.part + row * p.ldpart + col;
+        f32x4 v = *(const f32x4*)src;
+        for (int z = 1; z < p.split; ++z) v += *(const f32x4*)(src + (int64_t)z * p.M * p.ldpart);
+        linear_epilogue4<DT>(p.epi, v, row, col, p.N);
+    }
+}
+
+// Copies a 16-bit matrix whose rows cannot be read in 16-byte pieces (row length or stride not a
+// multiple of 8) into rows of cols8 = cols rounded up to 8, zeros behind.
+__global__ __launch_bounds__(256) void linear_pack_kernel(const uint16_t* __restrict__ src,
+                                                          int64_t ld, int rows, int cols,
+                                                          int cols8, uint16_t* __restrict__ dst) {
+    const int64_t total = (int64_t)rows * (cols8 / 2);
+    for (int64_t i = blockIdx.x * 256 + (int64_t)threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / (cols8 / 2);
+        const int c = (int)(i - r * (cols8 / 2)) * 2;
+        const uint16_t* s = src + r * ld + c;
+        const uint32_t lo = c < cols ? s[0] : 0, hi = c + 1 < cols ? s[1] : 0;
+        ((uint32_t*)dst)[i] = lo | hi << 16;
+    }
+}
+
+// dz = grad * act'(preact) as the 16-bit operand of the gradients' products, and this block's
+// column sums of it (fp32, unrounded).  An fp32 gradient is held as two 16-bit parts, dz = hi + lo
+// (lo = the rounding error of hi, itself rounded): 16 (bf16) or 22 (fp16) bits of it reach the
+// products, which then run over both parts.  A 16-bit gradient through an activation is rounded
+// once more to its own type: the products take nothing wider, and the error averages out over
+// the sums (each term's is at most half a step, the same as the output's own rounding).
+// Block (x, y): columns 64 x .. + 63, rows y, y + gridDim.y, ... in chunks of 16 rows.
+template <int DT>
+__global__ __launch_bounds__(256) void linear_dz_kernel(LinearDz p) {
+    __shared__ float red[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int col = blockIdx.x * 64 + lane;
+    float sum = 0.0f;
+    if (col < p.cols8) {
+        for (int64_t r = (int64_t)blockIdx.y * 4 + wave; r < p.M; r += (int64_t)gridDim.y * 4) {
+            float v = 0.0f;
+            if (col < p.N) {
+                v = p.grad_f32 ? ((const float*)p.grad)[r * p.ldg + col]
+                               : dt_to_f32<DT>(((const uint16_t*)p.grad)[r * p.ldg + col]);
+                if (p.act != MOE_ACT_NONE)
+                    v *= act_slope(dt_to_f32<DT>(p.preact[r * p.ldp + col]), p.act);
+            }
+            sum += v;
+            if (p.dz) {
+                const uint16_t hi = f32_to_dt<DT>(v);
+                p.dz[r * p.cols8 + col] = hi;
+                if (p.parts == 2) {
+                    const float h = dt_to_f32<DT>(hi);
+                    // an infinite or NaN part has no rounding error to keep
+                    p.dz[((int64_t)p.M + r) * p.cols8 + col] =
+                        f32_to_dt<DT>(h - h == 0.0f ? v - h : 0.0f);
+                }
+            }
+        }
+    }
+    if (!p.sums) return;
+    red[wave][lane] = sum;
+    __syncthreads();
+    if (wave == 0 && col < p.N)
+        p.sums[(int64_t)blockIdx.y * p.N + col] = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void linear_bias_kernel(const float* __restrict__ sums, int blocks,
+                                                          int N, uint16_t* __restrict__ out) {
+    const int col = blockIdx.x * 256 + threadIdx.x;
+    if (col >= N) return;
+    float v = 0.0f;
+    for (int b = 0; b < blocks; ++b) v += sums[(int64_t)b * N + col];
+    out[col] = f32_to_dt<DT>(v);
+}
+
+// ------------------------------------------------------------------------------------ host
+namespace {
+
+int grid_for(int64_t items, int per_block) {
+    const int64_t want = (items + per_block - 1) / per_block;
+    return (int)(want < 1 ? 1 : want > 16384 ? 16384 : want);
+}
+
+template <int DT, bool AC, bool BC>
+void launch_tiles(const LinearProduct& p, int cfg, hipStream_t s) {
+    const dim3 grid(p.tiles_m * p.tiles_n * p.split);
+    if (cfg == 0) linear_tile_kernel<DT, AC, BC, 256, 256, 2, 4><<<grid, 512, 0, s>>>(p);
+    else if (cfg == 1) linear_tile_kernel<DT, AC, BC, 128, 128, 2, 2><<<grid, 256, 0, s>>>(p);
+    else linear_tile_kernel<DT, AC, BC, 64, 64, 2, 2><<<grid, 256, 0, s>>>(p);
+}
+
+}  // namespace
+
+void linear_plan(LinearProduct& p) {
+    static const int bm[3] = {256, 128, 64};
+    const int stages = ((p.red + kBK - 1) / kBK) * p.parts;
+    auto tiles = [&](int c) {
+        return (int64_t)((p.M + bm[c] - 1) / bm[c]) * ((p.N + bm[c] - 1) / bm[c]);
+    };
+    int cfg = 0;
+    while (cfg < 2 && tiles(cfg) < 200) ++cfg;
+    int split = 1;
+    while (split < kLinearMaxSplit && tiles(cfg) * (split + 1) <= 512 && stages / (split + 1) >= 4) ++split;
+    p.cfg = cfg;
+    p.split = split;
+    p.tiles_m = (p.M + bm[cfg] - 1) / bm[cfg];
+    p.tiles_n = (p.N + bm[cfg] - 1) / bm[cfg];
+    p.ldpart = (p.N + 3) / 4 * 4;
+}
+
+size_t linear_part_bytes(const LinearProduct& p) {
+    return p.split > 1 ? (size_t)p.split * p.M * p.ldpart * 4 : 0;
+}
+
+hipError_t launch_linear_product(const LinearProduct& p, int dtype, hipStream_t s) {
+    auto go = [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        if (!p.a_cols && !p.b_cols) launch_tiles<DT, false, false>(p, p.cfg, s);
+        else if (!p.a_cols) launch_tiles<DT, false, true>(p, p.cfg, s);
+        else launch_tiles<DT, true, true>(p, p.cfg, s);
+        if (p.split > 1)
+            linear_reduce_kernel<DT><<<grid_for((int64_t)p.M * ((p.N + 3) / 4), 256), 256, 0, s>>>(p);
+    };
+    if (dtype == MOE_DT_BF16) go(std::integral_constant<int, MOE_DT_BF16>{});
+    else go(std::integral_constant<int, MOE_DT_FP16>{});
+    return hipGetLastError();
+}
+
+hipError_t launch_linear_pack(const uint16_t* src, int64_t ld, int rows, int cols, uint16_t* dst,
+                              hipStream_t s) {
+    const int cols8 = (cols + 7) / 8 * 8;
+    linear_pack_kernel<<<grid_for((int64_t)rows * (cols8 / 2), 256), 256, 0, s>>>(src, ld, rows, cols,
+                                                                              cols8, dst);
+    return hipGetLastError();
+}
+
+int linear_dz_blocks(int M) { return M < 4 ? 1 : M / 4 < 128 ? M / 4 : 128; }
+
+hipError_t launch_linear_dz(const LinearDz& p, int dtype, uint16_t* grad_bias, hipStream_t s) {
+    const int blocks = linear_dz_blocks(p.M);
+    const dim3 grid((p.cols8 + 63) / 64, blocks);
+    const int bgrid = (p.N + 255) / 256;
+    if (dtype == MOE_DT_BF16) {
+        linear_dz_kernel<MOE_DT_BF16><<<grid, 256, 0, s>>>(p);
+        if (grad_bias) linear_bias_kernel<MOE_DT_BF16><<<bgrid, 256, 0, s>>>(p.sums, blocks, p.N, grad_bias);
+    } else {
+        linear_dz_kernel<MOE_DT_FP16><<<grid, 256, 0, s>>>(p);
+        if (grad_bias) linear_bias_kernel<MOE_DT_FP16><<<bgrid, 256, 0, s>>>(p.sums, blocks, p.N, grad_bias);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace moe

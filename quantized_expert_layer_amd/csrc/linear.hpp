@@ -1,0 +1,229 @@
+// Tile product of the dense linear layer and of its gradients: C[i, j] = sum_r A[i, r] B[j, r]
+// over 16-bit operands, fp32 accumulators.  Each operand is stored either with the summed index
+// contiguous ("rows": A[i][r]) or with the output index contiguous ("cols": A[r][i]); the three
+// products of a linear layer are
+//   out[m, n] = sum_k a[m][k] w[n][k]      rows, rows
+//   da[m, k]  = sum_n dz[m][n] w[n][k]     rows, cols
+//   dw[n, k]  = sum_m dz[m][n] a[m][k]     cols, cols
+// so no operand is ever transposed in memory: the matrix core's operand layout (8 consecutive
+// summed indices per lane) comes from plain 16-byte LDS reads for "rows" and from the transposing
+// LDS read (ds_read_b64_tr_b16: 16 lanes read a 4 x 16 block and receive its columns) for "cols".
+#pragma once
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace moe {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma_dt(s16x8 a, s16x8 b, f32x4 c) {
+    if constexpr (DT == MOE_DT_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+template <int DT> __device__ __forceinline__ float dt_to_f32(uint16_t v) {
+    if constexpr (DT == MOE_DT_BF16) return __builtin_bit_cast(float, (uint32_t)v << 16);
+    else return (float)__builtin_bit_cast(f16, v);
+}
+template <int DT> __device__ __forceinline__ uint16_t f32_to_dt(float v) {   // nearest even
+    if constexpr (DT == MOE_DT_BF16) return __builtin_bit_cast(uint16_t, (__bf16)v);
+    else return __builtin_bit_cast(uint16_t, (f16)v);
+}
+
+// Activations on the fp32 sum and their slopes on the stored argument.  A NaN stays a NaN
+// (a maximum with 0 would drop it).
+__device__ __forceinline__ float gauss_cdf(float z) { return 0.5f * (1.0f + erff(z * 0.70710678f)); }
+__device__ __forceinline__ float act_value(float z, int act) {
+    switch (act) {
+        case MOE_ACT_RELU: return z < 0.0f ? 0.0f : z;
+        case MOE_ACT_SILU: return z / (1.0f + __expf(-z));
+        case MOE_ACT_GELU: return z * gauss_cdf(z);
+        default: return z;
+    }
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+    switch (act) {
+        case MOE_ACT_RELU: return z <= 0.0f ? 0.0f : 1.0f;
+        case MOE_ACT_SILU: {
+            const float s = 1.0f / (1.0f + __expf(-z));
+            return s * (1.0f + z * (1.0f - s));
+        }
+        case MOE_ACT_GELU: return gauss_cdf(z) + z * 0.39894228f * __expf(-0.5f * z * z);
+        default: return 1.0f;
+    }
+}
+
+constexpr int kBK = 64;                         // summed indices per stage
+
+// Tile of a block's index within one split.  Hardware block b runs on XCD b % 8, each with its own
+// L2: the tiles are cut into 8 contiguous ranges, one per XCD, and within a range run through
+// bands of 8 tile rows column by column, so that the tiles in flight on an XCD share operand rows.
+__device__ __forceinline__ void tile_of(const LinearProduct& p, int b, int& tm, int& tn) {
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int q = tiles / 8, rem = tiles % 8, x = b % 8, i = b / 8;
+    const int t = x * q + min(x, rem) + i;
+    const int band = t / (8 * p.tiles_n);
+    const int high = min(8, p.tiles_m - band * 8);
+    const int in = t - band * 8 * p.tiles_n;
+    tn = in / high;
+    tm = band * 8 + in % high;
+}
+
+// Address past every buffer resource: such a lane's load delivers zeros.
+constexpr uint32_t kOutside = 0x80000000u;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00020000);
+}
+
+// One operand's stage in LDS: OUT output indices x kBK summed indices.
+//   rows: row i (128 bytes, 8 chunks of 16) has its chunk c at position c ^ (i & 7), so the 16
+//         rows of a fragment read spread over all banks.
+//   cols: row r (2 OUT bytes) has its 32-byte pair p at position p ^ s(r), s(r) made of bits 0-1
+//         and 3-4 of r, the bits in which the rows of one transposing read differ.
+// The stage is filled by LDS-DMA (lane i of a load writes the wave's base + 16 i bytes), so the
+// swizzle is applied to the address each lane reads from memory.  Rows and chunks past the matrix
+// read as zeros (the buffer resource ends at the last valid element).
+template <int OUT, bool COLS, int WAVES>
+struct Operand {
+    static constexpr int kBytes = OUT * kBK * 2;
+    static constexpr int kLoads = kBytes / (1024 * WAVES);     // wave-wide loads per wave
+    static_assert(kLoads * 1024 * WAVES == kBytes, "a stage is a whole number of loads");
+    static constexpr int CR = COLS ? OUT / 8 : 8;              // chunks per LDS row
+    static constexpr uint32_t kPairMask = COLS ? CR / 2 - 1 : 0;
+
+    const uint16_t* base;    // first element of the tile's first stage
+    int64_t ld;
+    int outs;                // valid output indices of the tile (1..OUT)
+    int red;                 // summed indices in all
+    uint32_t off[kLoads];    // byte offset of each load within a stage
+    int kchunk[kLoads];      // rows: first summed index of the chunk within the stage
+
+    __device__ __forceinline__ void init(const uint16_t* m, int64_t ld_, int out0, int outs_total,
+                                         int red_, int wave, int lane) {
+        ld = ld_;
+        red = red_;
+        outs = min(OUT, outs_total - out0);
+        base = COLS ? m + out0 : m + (int64_t)out0 * ld;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int q = (wave * kLoads + i) * kWave + lane;
+            const int r = q / CR, pos = q % CR;
+            if constexpr (COLS) {
+                const uint32_t s = ((r & 3) | (((r >> 3) & 3) << 2)) & kPairMask;
+                const int c = pos ^ (int)(s << 1);
+                off[i] = c * 8 < outs ? (uint32_t)(r * (uint32_t)ld + c * 8) * 2u : kOutside;
+                kchunk[i] = 0;
+            } else {
+                const int c = pos ^ (r & 7);
+                off[i] = (uint32_t)(r * (uint32_t)ld + c * 8) * 2u;
+                kchunk[i] = c * 8;
+            }
+        }
+    }
+
+    // Loads stage k0 (first summed index) into LDS at dst (the operand's buffer of that stage).
+    __device__ __forceinline__ void load(int k0, const uint16_t* origin, char* dst, int wave) const {
+        const int left = red - k0;                           // >= 1
+        if constexpr (COLS) {
+            const int rows = min(left, kBK);
+            const uint32_t bytes = ((uint32_t)(rows - 1) * (uint32_t)ld + (uint32_t)outs) * 2u;
+            const auto rsrc = buffer_of(origin + (int64_t)k0 * ld, bytes);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rsrc, (lds_void*)(dst + (wave * kLoads + i) * 1024), 16, off[i], 0, 0, 0);
+        } else {
+            const uint32_t bytes = ((uint32_t)(outs - 1) * (uint32_t)ld + (uint32_t)left) * 2u;
+            const auto rsrc = buffer_of(origin + k0, bytes);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rsrc, (lds_void*)(dst + (wave * kLoads + i) * 1024), 16,
+                    kchunk[i] < left ? off[i] : kOutside, 0, 0, 0);
+        }
+    }
+
+    // Fragment of output indices out0 .. out0 + 15 and summed indices 32 ks .. 32 ks + 31.
+    static __device__ __forceinline__ s16x8 frag(const char* buf, int out0, int ks, int lane) {
+        if constexpr (COLS) {
+            const int r = ks * 32 + 8 * (lane >> 4) + ((lane >> 2) & 3);
+            const uint32_t s = (((lane >> 2) & 3) | ((lane >> 4) << 2)) & kPairMask;
+            const char* p = buf + r * (OUT * 2) + (((uint32_t)(out0 >> 4) ^ s) << 5) + (lane & 3) * 8;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * OUT * 2));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            const int r = out0 + (lane & 15);
+            const int c = (ks * 4 + (lane >> 4)) ^ (lane & 7);
+            return *(const s16x8*)(buf + r * 128 + c * 16);
+        }
+    }
+};
+
+// The linear layer's epilogue on four consecutive columns of one row.
+template <int DT>
+__device__ __forceinline__ void linear_epilogue4(const LinearEpilogue& e, f32x4 v, int64_t row,
+                                                 int col, int n) {
+    const int live = min(4, n - col);                   // >= 1
+    if (e.bias) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < live) v[i] += dt_to_f32<DT>(e.bias[col + i]);
+    }
+    if (e.preact) {
+        uint16_t* dst = e.preact + row * e.ldp + col;
+        if (live == 4 && e.vec_pre) {
+            uint2 o;
+            o.x = f32_to_dt<DT>(v[0]) | (uint32_t)f32_to_dt<DT>(v[1]) << 16;
+            o.y = f32_to_dt<DT>(v[2]) | (uint32_t)f32_to_dt<DT>(v[3]) << 16;
+            *(uint2*)dst = o;
+        } else {
+            for (int i = 0; i < live; ++i) dst[i] = f32_to_dt<DT>(v[i]);
+        }
+    }
+    if (e.act != MOE_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = act_value(v[i], e.act);
+    }
+    if (e.residual) {
+        const uint16_t* src = e.residual + row * e.ldr + col;
+        if (live == 4 && e.vec_res) {
+            const uint2 r = *(const uint2*)src;
+            v[0] += dt_to_f32<DT>((uint16_t)r.x);
+            v[1] += dt_to_f32<DT>((uint16_t)(r.x >> 16));
+            v[2] += dt_to_f32<DT>((uint16_t)r.y);
+            v[3] += dt_to_f32<DT>((uint16_t)(r.y >> 16));
+        } else {
+            for (int i = 0; i < live; ++i) v[i] += dt_to_f32<DT>(src[i]);
+        }
+    }
+    if (e.out_f32) {
+        float* dst = (float*)e.out + row * e.ldo + col;
+        if (live == 4 && e.vec_out) *(f32x4*)dst = v;
+        else for (int i = 0; i < live; ++i) dst[i] = v[i];
+    } else {
+        uint16_t* dst = (uint16_t*)e.out + row * e.ldo + col;
+        if (live == 4 && e.vec_out) {
+            uint2 o;
+            o.x = f32_to_dt<DT>(v[0]) | (uint32_t)f32_to_dt<DT>(v[1]) << 16;
+            o.y = f32_to_dt<DT>(v[2]) | (uint32_t)f32_to_dt<DT>(v[3]) << 16;
+            *(uint2*)dst = o;
+        } else {
+            for (int i = 0; i < live; ++i) dst[i] = f32_to_dt<DT>(v[i]);
+        }
+    }
+}
+
+}  // namespace moe

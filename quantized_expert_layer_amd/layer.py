@@ -18,10 +18,11 @@ import numpy as np
 import ctypes
 
 from . import (ACTS, GATES, MOE_DECODE_MAX_ROWS, MOE_DECODE_MAX_TOKENS, WTYPES, MoEError, _ptr,
-               _stream, lib, moe_decode_layer, moe_decode_layer_shared,
+               _stream, lib, moe_combine_backward, moe_decode_layer, moe_decode_layer_shared,
                moe_decode_shared_workspace_size, moe_decode_workspace_size,
                moe_gemm_workspace_size, moe_grouped_gemm_wq, moe_grouped_gemm_wq_rows,
-               moe_pack_wq, moe_permute, moe_permute_workspace_size, moe_route_topk,
+               moe_pack_wq, moe_permute, moe_permute_workspace_size, moe_route_backward,
+               moe_route_topk,
                moe_unpermute_combine, new_output)
 
 
@@ -252,6 +253,28 @@ class DeviceLayer:
         moe_unpermute_combine(b["y"], b["inv"], None if gate_in_gemm else b["w"], addend, T,
                               self.k, out=b["out"], stream=stream)
         return b["out"]
+
+    def router_backward(self, grad_out, logits, ws: Workspace, active=None, counts=None,
+                        tokens=None, coef: float = 0.0, grad_loss=None, seq_offsets=None,
+                        grad_logits=None, stream=None):
+        """Gradient fp32 [T, E] of the router logits, the experts frozen: through the gate weights
+        of the forward() that filled `ws` (called with gate_in_gemm=False and the same logits and
+        active, so that ws holds each expert row unscaled), given the gradient grad_out fp16 [T, d]
+        of its output; with counts and tokens (moe_balance_loss) also through the balance loss
+        coef, grad_loss and seq_offsets belong to."""
+        T = ws.T
+        if self.uses_decode(T, gate_in_gemm=False):
+            raise ValueError("the decode call keeps no expert rows: use decode=None or False")
+        if grad_out.shape != (T, self.d) or logits.shape != (T, self.E):
+            raise ValueError(f"expected grad_out {(T, self.d)} and logits {(T, self.E)}, got "
+                             f"{tuple(grad_out.shape)} and {tuple(logits.shape)}")
+        b = ws.bufs
+        grad_w, _ = moe_combine_backward(grad_out, b["y"], b["inv"], b["w"], need_y=False,
+                                         stream=stream)
+        return moe_route_backward(logits, b["ids"], gate_mode=self.gate_mode, topk_w=b["w"],
+                                  grad_w=grad_w, active=active, counts=counts, tokens=tokens,
+                                  coef=coef, grad_loss=grad_loss, seq_offsets=seq_offsets,
+                                  grad_logits=grad_logits, stream=stream)
 
     # ------------------------------------------------------------------ cached launch plan
     def plan(self, ws: Workspace, x, logits, weights=None, gate_in_gemm: bool = True,
