@@ -605,46 +605,52 @@ def _place(ref, stream):
     return torch.cuda.stream(stream)
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _here(dev):
+    """Handle of dev's current stream (asked for without building a Stream object: that costs as
+    much host time as the call itself)."""
+    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    return _torch().cuda.current_stream(dev).cuda_stream if raw is None else raw(dev.index)
+
+
+def _refuse(t, dtype, name, shape, dev):
+    """Raises for the first thing that is wrong with t's type, device or shape."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _dense(t, dtype, name, shape, dev):
-    """A dense device tensor of exactly this type, shape and device."""
+    """Address of a dense device tensor of exactly this type, shape and device (None: None)."""
     if t is None:
-        return
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+        return None
+    if not (getattr(t, "dtype", None) is dtype and t.shape == shape and t.device == dev):
+        _refuse(t, dtype, name, shape, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _rows(t, dtype, name, shape, dev):
-    """Row stride of a device matrix of this type and shape whose rows are contiguous (0: None)."""
+    """(address, row stride) of a device matrix of this type and shape whose rows are contiguous
+    ((None, 0): None)."""
     if t is None:
-        return 0
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+        return None, 0
+    if not (getattr(t, "dtype", None) is dtype and t.shape == shape and t.device == dev):
+        _refuse(t, dtype, name, shape, dev)
     rows, cols = shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
     if rows <= 1 or cols == 0:
-        if cols > 1 and t.stride(1) != 1:
-            raise ValueError(f"{name}: rows must be contiguous")
-        return cols
-    if (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
-        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
-    return t.stride(0)
+        return t.data_ptr(), cols
+    if ld < cols:
+        raise ValueError(f"{name}: rows must not overlap")
+    return t.data_ptr(), ld
 
 
 def _dt(dtype, name):
@@ -665,13 +671,13 @@ def _linear_act(act):
 
 
 def _workspace(need, ws, dev):
-    torch = _torch()
+    """(ws, its address, its bytes), allocated if None."""
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _need(ws, torch.uint8, "ws")
-    if ws.device != dev:
-        raise ValueError(f"ws: expected a tensor on {dev}, got {ws.device}")
-    return ws
+        if not need:
+            return None, None, 0
+        ws = _torch().empty(need, dtype=_torch().uint8, device=dev)
+        return ws, ws.data_ptr(), need
+    return ws, _dense(ws, _torch().uint8, "ws", (ws.numel(),), dev), ws.numel()
 
 
 def moe_linear_workspace_size(M, N, K, lda=None, ldw=None):
@@ -699,18 +705,17 @@ def moe_linear(a, w, bias=None, act="none", residual=None, out=None, out_dtype=N
         elif out_dtype is not None and out.dtype != out_dtype:
             raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
         od = DT_FP32 if out.dtype == torch.float32 else _dt(out.dtype, "out")
-        lda = _rows(a, dtype, "a", (M, K), dev)
-        ldw = _rows(w, dtype, "w", (N, K), dev)
-        ldr = _rows(residual, dtype, "residual", (M, N), dev)
-        ldo = _rows(out, out.dtype, "out", (M, N), dev)
-        ldp = _rows(preact, dtype, "preact", (M, N), dev)
-        _dense(bias, dtype, "bias", (N,), dev)
+        pa, lda = _rows(a, dtype, "a", (M, K), dev)
+        pw, ldw = _rows(w, dtype, "w", (N, K), dev)
+        pr, ldr = _rows(residual, dtype, "residual", (M, N), dev)
+        po, ldo = _rows(out, out.dtype, "out", (M, N), dev)
+        pp, ldp = _rows(preact, dtype, "preact", (M, N), dev)
+        pb = _dense(bias, dtype, "bias", (N,), dev)
         ac = _linear_act(act)
         L = lib()
-        ws = _workspace(L.moe_linear_workspace_size(M, N, K, lda, ldw), ws, dev)
-        _check("moe_linear", L.moe_linear(
-            _at(a), lda, _at(w), ldw, _at(bias), _at(residual), ldr, M, N, K, dt, ac, _at(out),
-            ldo, od, _at(preact), ldp, _at(ws), 0 if ws is None else ws.numel(), _stream(None)))
+        ws, pws, nws = _workspace(L.moe_linear_workspace_size(M, N, K, lda, ldw), ws, dev)
+        _check("moe_linear", L.moe_linear(pa, lda, pw, ldw, pb, pr, ldr, M, N, K, dt, ac, po, ldo,
+                                          od, pp, ldp, pws, nws, _here(dev)))
     return out
 
 
@@ -744,20 +749,19 @@ def moe_linear_backward(grad_out, a, w, act="none", preact=None, need_a=True, ne
             grad_bias = new_output((N,), dtype, dev)
         gd = grad_out.dtype
         gdt = DT_FP32 if gd == torch.float32 else _dt(gd, "grad_out")
-        ldg = _rows(grad_out, gd, "grad_out", (M, N), dev)
-        lda = _rows(a, dtype, "a", (M, K), dev)
-        ldw = _rows(w, dtype, "w", (N, K), dev)
-        ldp = _rows(preact, dtype, "preact", (M, N), dev)
-        _dense(grad_a, dtype, "grad_a", (M, K), dev)
-        _dense(grad_w, dtype, "grad_w", (N, K), dev)
-        _dense(grad_bias, dtype, "grad_bias", (N,), dev)
+        pg, ldg = _rows(grad_out, gd, "grad_out", (M, N), dev)
+        pa, lda = _rows(a, dtype, "a", (M, K), dev)
+        pw, ldw = _rows(w, dtype, "w", (N, K), dev)
+        pp, ldp = _rows(preact, dtype, "preact", (M, N), dev)
+        pga = _dense(grad_a, dtype, "grad_a", (M, K), dev)
+        pgw = _dense(grad_w, dtype, "grad_w", (N, K), dev)
+        pgb = _dense(grad_bias, dtype, "grad_bias", (N,), dev)
         L = lib()
-        ws = _workspace(L.moe_linear_backward_workspace_size(M, N, K, lda, ldw, ldg, gdt, ac), ws,
-                        dev)
+        need = L.moe_linear_backward_workspace_size(M, N, K, lda, ldw, ldg, gdt, ac)
+        ws, pws, nws = _workspace(need, ws, dev)
         _check("moe_linear_backward", L.moe_linear_backward(
-            _at(grad_out), ldg, gdt, _at(preact), ldp, _at(a), lda, _at(w), ldw, M, N, K, dt, ac,
-            _at(grad_a), _at(grad_w), _at(grad_bias), _at(ws), 0 if ws is None else ws.numel(),
-            _stream(None)))
+            pg, ldg, gdt, pp, ldp, pa, lda, pw, ldw, M, N, K, dt, ac, pga, pgw, pgb, pws, nws,
+            _here(dev)))
     return grad_a, grad_w, grad_bias
 
 
@@ -766,14 +770,14 @@ def moe_balance_workspace_size(T, E, S=1):
 
 
 def _segments(seq_offsets, dev):
-    """Number of segments of seq_offsets (int32 [S + 1], or None: one)."""
+    """(number of segments, address) of seq_offsets (int32 [S + 1], or None: one segment)."""
     if seq_offsets is None:
-        return 1
+        return 1, None
     S = seq_offsets.numel() - 1
-    _dense(seq_offsets, _torch().int32, "seq_offsets", (S + 1,), dev)
+    ps = _dense(seq_offsets, _torch().int32, "seq_offsets", (S + 1,), dev)
     if S < 1:
         raise ValueError("seq_offsets needs at least two entries")
-    return S
+    return S, ps
 
 
 def moe_balance_loss(logits, topk_ids, coef, active=None, seq_offsets=None, loss=None, counts=None,
@@ -785,7 +789,7 @@ def moe_balance_loss(logits, topk_ids, coef, active=None, seq_offsets=None, loss
     k = topk_ids.shape[1]
     dev = logits.device
     with _place(logits, stream):
-        S = _segments(seq_offsets, dev)
+        S, ps = _segments(seq_offsets, dev)
         if loss is None:
             loss = new_output((1,), torch.float32, dev)
         if counts is None:
@@ -794,19 +798,18 @@ def moe_balance_loss(logits, topk_ids, coef, active=None, seq_offsets=None, loss
             probs = new_output((S, E), torch.float32, dev)
         if tokens is None:
             tokens = new_output((S,), torch.int32, dev)
-        _dense(logits, torch.float32, "logits", (T, E), dev)
-        _dense(topk_ids, torch.int32, "topk_ids", (T, k), dev)
-        _dense(active, torch.uint8, "active", (T,), dev)
-        _dense(loss, torch.float32, "loss", (1,), dev)
-        _dense(counts, torch.int32, "counts", (S, E), dev)
-        _dense(probs, torch.float32, "probs", (S, E), dev)
-        _dense(tokens, torch.int32, "tokens", (S,), dev)
+        f32, i32 = torch.float32, torch.int32
+        pl = _dense(logits, f32, "logits", (T, E), dev)
+        pi = _dense(topk_ids, i32, "topk_ids", (T, k), dev)
+        pa = _dense(active, torch.uint8, "active", (T,), dev)
+        po = _dense(loss, f32, "loss", (1,), dev)
+        pc = _dense(counts, i32, "counts", (S, E), dev)
+        pp = _dense(probs, f32, "probs", (S, E), dev)
+        pt = _dense(tokens, i32, "tokens", (S,), dev)
         L = lib()
-        ws = _workspace(L.moe_balance_workspace_size(T, E, S), ws, dev)
+        ws, pws, nws = _workspace(L.moe_balance_workspace_size(T, E, S), ws, dev)
         _check("moe_balance_loss", L.moe_balance_loss(
-            _at(logits), _at(topk_ids), _at(active), _at(seq_offsets), S, T, E, k, float(coef),
-            _at(loss), _at(counts), _at(probs), _at(tokens), _at(ws),
-            0 if ws is None else ws.numel(), _stream(None)))
+            pl, pi, pa, ps, S, T, E, k, float(coef), po, pc, pp, pt, pws, nws, _here(dev)))
     return loss, counts, probs, tokens
 
 
@@ -821,22 +824,22 @@ def moe_route_backward(logits, topk_ids, gate_mode="topk", topk_w=None, grad_w=N
     k = topk_ids.shape[1]
     dev = logits.device
     with _place(logits, stream):
-        S = _segments(seq_offsets, dev)
+        S, ps = _segments(seq_offsets, dev)
         if grad_logits is None:
             grad_logits = new_output((T, E), torch.float32, dev)
-        _dense(logits, torch.float32, "logits", (T, E), dev)
-        _dense(topk_ids, torch.int32, "topk_ids", (T, k), dev)
-        _dense(topk_w, torch.float32, "topk_w", (T, k), dev)
-        _dense(grad_w, torch.float32, "grad_w", (T, k), dev)
-        _dense(active, torch.uint8, "active", (T,), dev)
-        _dense(counts, torch.int32, "counts", (S, E), dev)
-        _dense(tokens, torch.int32, "tokens", (S,), dev)
-        _dense(grad_loss, torch.float32, "grad_loss", (1,), dev)
-        _dense(grad_logits, torch.float32, "grad_logits", (T, E), dev)
+        f32, i32 = torch.float32, torch.int32
+        pl = _dense(logits, f32, "logits", (T, E), dev)
+        pi = _dense(topk_ids, i32, "topk_ids", (T, k), dev)
+        pw = _dense(topk_w, f32, "topk_w", (T, k), dev)
+        pg = _dense(grad_w, f32, "grad_w", (T, k), dev)
+        pa = _dense(active, torch.uint8, "active", (T,), dev)
+        pc = _dense(counts, i32, "counts", (S, E), dev)
+        pt = _dense(tokens, i32, "tokens", (S,), dev)
+        pgl = _dense(grad_loss, f32, "grad_loss", (1,), dev)
+        po = _dense(grad_logits, f32, "grad_logits", (T, E), dev)
         _check("moe_route_backward", lib().moe_route_backward(
-            _at(logits), _at(topk_ids), _at(topk_w), _at(grad_w), _at(active), _at(seq_offsets), S,
-            T, E, k, GATES.get(gate_mode, gate_mode), _at(counts), _at(tokens), float(coef),
-            _at(grad_loss), _at(grad_logits), _stream(None)))
+            pl, pi, pw, pg, pa, ps, S, T, E, k, GATES.get(gate_mode, gate_mode), pc, pt,
+            float(coef), pgl, po, _here(dev)))
     return grad_logits
 
 
@@ -854,17 +857,16 @@ def moe_combine_backward(grad_out, y_perm, inv_perm, topk_w, need_w=True, need_y
             grad_w = new_output((T, k), torch.float32, dev)
         if grad_y is None and need_y:
             grad_y = new_output((R, d), torch.float16, dev)
-        _dense(grad_out, torch.float16, "grad_out", (T, d), dev)
-        _dense(y_perm, torch.float16, "y_perm", (R, d), dev)
+        pg = _dense(grad_out, torch.float16, "grad_out", (T, d), dev)
+        py = _dense(y_perm, torch.float16, "y_perm", (R, d), dev)
         if R < T * k:
             raise ValueError(f"y_perm: needs at least {T * k} rows, has {R}")
-        _dense(inv_perm, torch.int32, "inv_perm", (T * k,), dev)
-        _dense(topk_w, torch.float32, "topk_w", (T, k), dev)
-        _dense(grad_w, torch.float32, "grad_w", (T, k), dev)
-        _dense(grad_y, torch.float16, "grad_y", (R, d), dev)
+        pi = _dense(inv_perm, torch.int32, "inv_perm", (T * k,), dev)
+        pw = _dense(topk_w, torch.float32, "topk_w", (T, k), dev)
+        pgw = _dense(grad_w, torch.float32, "grad_w", (T, k), dev)
+        pgy = _dense(grad_y, torch.float16, "grad_y", (R, d), dev)
         _check("moe_combine_backward", lib().moe_combine_backward(
-            _at(grad_out), _at(y_perm), _at(inv_perm), _at(topk_w), T, k, d, _at(grad_w),
-            _at(grad_y), _stream(None)))
+            pg, py, pi, pw, T, k, d, pgw, pgy, _here(dev)))
     return grad_w, grad_y
 
 

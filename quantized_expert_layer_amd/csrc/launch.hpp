@@ -148,7 +148,7 @@ struct LinearProduct {       // C[i, j] = sum over parts and r < red of A[i, r] 
     const uint16_t* a;
     const uint16_t* b;
     int64_t lda, ldb;
-    int64_t a_part, b_part;  // elements from one part of the summed index to the next
+    int64_t a_part;          // elements from A's first part of the summed index to its second
     int a_cols, b_cols;      // operand stored with its output index contiguous
     int a_outs, b_outs;      // output indices the operands hold (>= M, N: padded copies)
     int red, b_red, parts;   // summed indices per part (b_red: rows B really has); 1 or 2 parts

@@ -6,8 +6,11 @@
 namespace moe {
 
 // ------------------------------------------------------------------------------------
-// Tile product.  A block computes BM x BN outputs with WM x WN waves; a stage (64 summed
-// indices) of both operands is loaded into LDS while the previous one is multiplied.
+// Tile product.  A block computes BM x BN outputs with WM x WN waves, 64 summed indices (a stage)
+// at a time.  A stage's two halves of 32 alternate between two fragment sets: while one half is
+// multiplied the next one is read from LDS, across the stages too, so the matrix cores wait for no
+// LDS read.  The barrier therefore sits in the middle of a stage: behind it the next stage has
+// landed, and this stage's buffer, its second half read by then, takes the stage after the next.
 // ------------------------------------------------------------------------------------
 template <int DT, bool ACOLS, bool BCOLS, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearProduct p) {
@@ -16,7 +19,8 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearProduct
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;        // 16x16 subtiles per wave
     using OA = Operand<BM, ACOLS, W>;
     using OB = Operand<BN, BCOLS, W>;
-    __shared__ __attribute__((aligned(1024))) char lds[2 * (OA::kBytes + OB::kBytes)];
+    constexpr int kStage = OA::kBytes + OB::kBytes;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
 
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -43,35 +47,98 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearProduct
     const int per = (p.red + kBK - 1) / kBK;
     const int total = per * p.parts;
     const int s0 = (int)((int64_t)total * z / p.split), s1 = (int)((int64_t)total * (z + 1) / p.split);
-    auto load = [&](int s, int buf) {
-        const int part = s >= per ? 1 : 0;
-        const int k0 = (s - part * per) * kBK;
-        char* dst = lds + buf * (OA::kBytes + OB::kBytes);
-        oa.load(k0, oa.base + part * p.a_part, dst, wave);
-        ob.load(k0, ob.base + part * p.b_part, dst + OA::kBytes, wave);
+    constexpr int NL = OA::kLoads + OB::kLoads;
+    struct Stage {
+        __amdgpu_buffer_rsrc_t a, b;
+        int left, left_b;
     };
-    if (s0 < s1) load(s0, 0);
-    for (int s = s0; s < s1; ++s) {
-        const int buf = (s - s0) & 1;
-        __builtin_amdgcn_s_waitcnt(0x0f70);                    // vmcnt(0): this wave's loads landed
-        __builtin_amdgcn_s_barrier();                          // and everyone's; other buffer free
-        __builtin_amdgcn_sched_barrier(0);
-        if (s + 1 < s1) load(s + 1, buf ^ 1);
-        const char* la = lds + buf * (OA::kBytes + OB::kBytes);
-        const char* lb = la + OA::kBytes;
+    // The stages in order, each block of an XCD starting an eighth further on and wrapping round:
+    // at any moment the XCDs then read different parts of the rows, which spreads their requests
+    // over the memory channels (rows a power of two apart share few of them); blocks of one XCD stay
+    // together and share its L2.  Stages past the last read as zeros, so that the loop below has
+    // no branch and runs a whole number of rounds through the buffers.
+    int remain = s1 - s0, cur = s0 + (int)((int64_t)(blockIdx.x % 8) * remain / 8);
+    auto next_stage = [&]() {
+        const int part = cur >= per ? 1 : 0;
+        const int k = cur - part * per;
+        const int left = p.red - k * kBK, left_b = p.b_red - k * kBK;
+        const Stage st{oa.stage(oa.base + part * p.a_part + k * oa.step(), left, remain > 0),
+                       ob.stage(ob.base + k * ob.step(), left_b, remain > 0), left, left_b};
+        --remain;
+        cur = cur + 1 < s1 ? cur + 1 : s0;
+        return st;
+    };
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)lds;
+    auto load = [&](const Stage& st, int i, int buf) {
+        const uint32_t dst = lds0 + buf * kStage;
+        if (i < OA::kLoads) oa.load(st.a, i, st.left, dst, wave);
+        else ob.load(st.b, i - OA::kLoads, st.left_b, dst + OA::kBytes, wave);
+    };
+    typename OA::template Reader<TM> ra;
+    typename OB::template Reader<TN> rb;
+    ra.init(wm * TM * 16, lane);
+    rb.init(wn * TN * 16, lane);
+    // fragment f (0 .. TN-1: of B, then of A) of half ks of the stage in buffer buf
+    auto read = [&](s16x8 (&fa)[TM], s16x8 (&fb)[TN], int f, int buf, int ks) {
+        if (f < TN) fb[f] = rb.read(lds + buf * kStage + OA::kBytes, f, ks);
+        else fa[f - TN] = ra.read(lds + buf * kStage, f - TN, ks);
+    };
+    // Multiplies the half in (ca, cb) in TM groups of TN products and reads half ks of buffer buf
+    // into (na, nb); `more`: also loads stage st into buffer `into`.  Loads and reads are spread
+    // over the groups: issued in one go they fill the memory and LDS queues and stall the wave
+    // behind them (1000 cycles a stage in which nothing multiplied).
+    auto half = [&](const s16x8 (&ca)[TM], const s16x8 (&cb)[TN], s16x8 (&na)[TM], s16x8 (&nb)[TN],
+                    int buf, int ks, bool more, const Stage& st, int into) {
+        constexpr int GR = TM - TM / 4;                        // groups with reads
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            s16x8 fa[TM], fb[TN];
+        for (int g = 0; g < TM; ++g) {
+            if (more) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i) fa[i] = OA::frag(la, (wm * TM + i) * 16, ks, lane);
+                for (int i = g * NL / TM; i < (g + 1) * NL / TM; ++i) load(st, i, into);
+            }
+            if (g < GR) {
 #pragma unroll
-            for (int j = 0; j < TN; ++j) fb[j] = OB::frag(lb, (wn * TN + j) * 16, ks, lane);
+                for (int f = g * (TM + TN) / GR; f < (g + 1) * (TM + TN) / GR; ++f)
+                    read(na, nb, f, buf, ks);
+            }
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TN; ++j) acc[i][j] = mfma_dt<DT>(fb[j], fa[i], acc[i][j]);
+            for (int j = 0; j < TN; ++j) acc[g][j] = mfma_dt<DT>(cb[j], ca[g], acc[g][j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
+    };
+    // Behind the barrier all loads issued before it, by any wave, have landed and all LDS reads
+    // have been served.
+    auto land = [&]() {
         __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0x0070);                    // vmcnt(0) lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (s0 < s1) {
+        s16x8 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
+        Stage st = next_stage();
+#pragma unroll
+        for (int i = 0; i < NL; ++i) load(st, i, 0);
+        st = next_stage();
+#pragma unroll
+        for (int i = 0; i < NL; ++i) load(st, i, 1);
+        static_assert(NL < 16, "vmcnt");
+        __builtin_amdgcn_s_waitcnt(0x0f70 | NL);               // the first stage
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < TM + TN; ++f) read(fa0, fb0, f, 0, 0);
+        for (int s = s0; s < s1; s += 2) {
+            half(fa0, fb0, fa1, fb1, 0, 1, false, st, 0);
+            st = next_stage();
+            land();
+            half(fa1, fb1, fa0, fb0, 1, 0, true, st, 0);
+            half(fa0, fb0, fa1, fb1, 1, 1, false, st, 0);
+            st = next_stage();
+            land();
+            half(fa1, fb1, fa0, fb0, 0, 0, true, st, 1);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0070);                    // nothing may land in LDS any more
     }
 
     // The accumulators (lane: row lane & 15 of a subtile, columns 4 (lane >> 4) .. + 3) leave
@@ -215,7 +282,7 @@ void linear_plan(LinearProduct& p) {
     int cfg = 0;
     while (cfg < 2 && tiles(cfg) < 200) ++cfg;
     int split = 1;
-    while (split < kLinearMaxSplit && tiles(cfg) * (split + 1) <= 512 && stages / (split + 1) >= 4) ++split;
+    while (split < kLinearMaxSplit && tiles(cfg) * (split + 1) <= 320 && stages / (split + 1) >= 8) ++split;
     p.cfg = cfg;
     p.split = split;
     p.tiles_m = (p.M + bm[cfg] - 1) / bm[cfg];

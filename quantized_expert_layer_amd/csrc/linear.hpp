@@ -64,7 +64,7 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     }
 }
 
-constexpr int kBK = 64;                         // summed indices per stage
+constexpr int kBK = 64;                         // summed indices per stage: a 128-byte line of a row
 
 // Tile of a block's index within one split.  Hardware block b runs on XCD b % 8, each with its own
 // L2: the tiles are cut into 8 contiguous ranges, one per XCD, and within a range run through
@@ -87,20 +87,30 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, ui
     return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00020000);
 }
 
+// 16 bytes per lane from memory straight into LDS: lane i's to lds + 16 i.  Issued as an instruction
+// of its own: with the builtin the compiler waits for every such load in flight (vmcnt 0) before
+// each transposing LDS read, which it cannot tell apart from them.  It has no register result; the
+// kernel's own wait and barrier order it before the reads of its buffer.  (The no-op is the wait
+// state an LDS load needs after M0 is written; nothing else in these kernels uses M0.)
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t rsrc, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 : : "v"(off), "s"(rsrc), "s"(lds) : "memory");
+}
+
 // One operand's stage in LDS: OUT output indices x kBK summed indices.
-//   rows: row i (128 bytes, 8 chunks of 16) has its chunk c at position c ^ (i & 7), so the 16
-//         rows of a fragment read spread over all banks.
+//   rows: row i (128 bytes, 8 chunks of 16) has its chunk c at position c ^ (i & 7), so the rows of
+//         a fragment read spread over all banks.
 //   cols: row r (2 OUT bytes) has its 32-byte pair p at position p ^ s(r), s(r) made of bits 0-1
 //         and 3-4 of r, the bits in which the rows of one transposing read differ.
-// The stage is filled by LDS-DMA (lane i of a load writes the wave's base + 16 i bytes), so the
-// swizzle is applied to the address each lane reads from memory.  Rows and chunks past the matrix
-// read as zeros (the buffer resource ends at the last valid element).
+// The stage is filled by LDS-DMA, whose lanes write consecutive places, so the swizzle is applied
+// to the address each lane reads from memory.  Rows and chunks past the matrix read as zeros (the
+// buffer resource ends at the last valid element).
 template <int OUT, bool COLS, int WAVES>
 struct Operand {
     static constexpr int kBytes = OUT * kBK * 2;
     static constexpr int kLoads = kBytes / (1024 * WAVES);     // wave-wide loads per wave
     static_assert(kLoads * 1024 * WAVES == kBytes, "a stage is a whole number of loads");
-    static constexpr int CR = COLS ? OUT / 8 : 8;              // chunks per LDS row
+    static constexpr int CR = COLS ? OUT / 8 : kBK / 8;        // chunks per LDS row
     static constexpr uint32_t kPairMask = COLS ? CR / 2 - 1 : 0;
 
     const uint16_t* base;    // first element of the tile's first stage
@@ -133,43 +143,52 @@ struct Operand {
         }
     }
 
-    // Loads stage k0 (first summed index) into LDS at dst (the operand's buffer of that stage).
-    __device__ __forceinline__ void load(int k0, const uint16_t* origin, char* dst, int wave) const {
-        const int left = red - k0;                           // >= 1
-        if constexpr (COLS) {
-            const int rows = min(left, kBK);
-            const uint32_t bytes = ((uint32_t)(rows - 1) * (uint32_t)ld + (uint32_t)outs) * 2u;
-            const auto rsrc = buffer_of(origin + (int64_t)k0 * ld, bytes);
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    rsrc, (lds_void*)(dst + (wave * kLoads + i) * 1024), 16, off[i], 0, 0, 0);
-        } else {
-            const uint32_t bytes = ((uint32_t)(outs - 1) * (uint32_t)ld + (uint32_t)left) * 2u;
-            const auto rsrc = buffer_of(origin + k0, bytes);
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    rsrc, (lds_void*)(dst + (wave * kLoads + i) * 1024), 16,
-                    kchunk[i] < left ? off[i] : kOutside, 0, 0, 0);
-        }
+    // The loads of the stage that starts at `from` with `left` summed indices still to come: the
+    // buffer resource (empty unless `live`: zeros, and nothing is read), then load i of kLoads into
+    // the operand's buffer at LDS address dst.
+    __device__ __forceinline__ int64_t step() const { return COLS ? kBK * ld : kBK; }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t stage(const uint16_t* from, int left,
+                                                            bool live) const {
+        const uint32_t n = COLS ? (uint32_t)(min(left, kBK) - 1) * (uint32_t)ld + (uint32_t)outs
+                                : (uint32_t)(outs - 1) * (uint32_t)ld + (uint32_t)left;
+        return buffer_of(from, live ? n * 2u : 0u);
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rsrc, int i, int left, uint32_t dst,
+                                         int wave) const {
+        load_lds16(rsrc, COLS || kchunk[i] < left ? off[i] : kOutside, dst + (wave * kLoads + i) * 1024);
     }
 
-    // Fragment of output indices out0 .. out0 + 15 and summed indices 32 ks .. 32 ks + 31.
-    static __device__ __forceinline__ s16x8 frag(const char* buf, int out0, int ks, int lane) {
-        if constexpr (COLS) {
-            const int r = ks * 32 + 8 * (lane >> 4) + ((lane >> 2) & 3);
-            const uint32_t s = (((lane >> 2) & 3) | ((lane >> 4) << 2)) & kPairMask;
-            const char* p = buf + r * (OUT * 2) + (((uint32_t)(out0 >> 4) ^ s) << 5) + (lane & 3) * 8;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * OUT * 2));
-            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        } else {
-            const int r = out0 + (lane & 15);
-            const int c = (ks * 4 + (lane >> 4)) ^ (lane & 7);
-            return *(const s16x8*)(buf + r * 128 + c * 16);
+    // A wave's FR fragments of 16 output indices from `first` (a multiple of 16 FR) on: the offsets
+    // of this lane's pieces within a stage's buffer.
+    template <int FR>
+    struct Reader {
+        uint32_t at[COLS ? FR : 2];
+        __device__ __forceinline__ void init(int first, int lane) {
+            if constexpr (COLS) {
+                const int r = 8 * (lane >> 4) + ((lane >> 2) & 3);
+                const uint32_t s = (((lane >> 2) & 3) | ((lane >> 4) << 2)) & kPairMask;
+#pragma unroll
+                for (int f = 0; f < FR; ++f)
+                    at[f] = r * (OUT * 2) + (((uint32_t)((first >> 4) + f) ^ s) << 5) + (lane & 3) * 8;
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+                    at[ks] = (first + (lane & 15)) * (kBK * 2) +
+                             (((ks * 4 + (lane >> 4)) ^ (lane & 7)) * 16);
+            }
         }
-    }
+        // Fragment f, summed indices 32 ks .. 32 ks + 31.
+        __device__ __forceinline__ s16x8 read(const char* buf, int f, int ks) const {
+            if constexpr (COLS) {
+                const char* p = buf + at[f] + ks * (32 * OUT * 2);
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * OUT * 2));
+                return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            } else {
+                return *(const s16x8*)(buf + at[ks] + f * (16 * kBK * 2));
+            }
+        }
+    };
 };
 
 // The linear layer's epilogue on four consecutive columns of one row.

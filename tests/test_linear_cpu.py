@@ -101,7 +101,6 @@ def test_workspace_sizes():
     # rows that cannot be read in 16-byte pieces are copied, rounded up to 8 columns
     assert size(5, 9, 63) >= 2 * 64 * (5 + 9)
     assert size(5, 9, 64, lda=65, ldw=64) >= 2 * 64 * 5
-    assert size(3840, 4096, 1024) == 0                    # aligned, and enough tiles without a split
     back = q.moe_linear_backward_workspace_size
     assert back(100, 64, 64, grad_f32=True) >= 2 * 2 * 100 * 64       # two 16-bit parts
     assert back(100, 60, 64) >= 2 * 100 * 64                          # gradient rows rounded up
