@@ -717,7 +717,7 @@ LinearBackward linear_backward(int32_t M, int32_t N, int32_t K, int64_t lda, int
 void grad_out_epilogue(moe::LinearEpilogue& e, uint16_t* out, int32_t K) {
     e.out = out;
     e.ldo = K;
-    e.vec_out = K % 4 == 0;
+    e.vec = K % 8 == 0;
 }
 
 }  // namespace
@@ -779,9 +779,7 @@ int32_t moe_linear(const uint16_t* a, int64_t lda, const uint16_t* w, int64_t ld
     e.ldo = ldo;
     e.out_f32 = out_dtype == MOE_DT_FP32;
     e.act = act;
-    e.vec_out = ldo % 4 == 0;
-    e.vec_res = ldr % 4 == 0;
-    e.vec_pre = ldp % 4 == 0;
+    e.vec = ldo % 8 == 0 && (!residual || ldr % 8 == 0) && (!preact || ldp % 8 == 0);
     return hip_status(moe::launch_linear_product(p, dtype, s));
 }
 

@@ -141,7 +141,7 @@ struct LinearEpilogue {      // out = act(sum + bias) + residual; preact = sum +
     void* out;               // 16-bit of the operands' type, or fp32
     int64_t ldo;
     int out_f32, act;
-    int vec_out, vec_res, vec_pre;   // four columns of a row are one aligned access
+    int vec;                 // eight columns of a row are 16-byte aligned in every matrix here
 };
 
 struct LinearProduct {       // C[i, j] = sum over parts and r < red of A[i, r] B[j, r]
@@ -156,6 +156,7 @@ struct LinearProduct {       // C[i, j] = sum over parts and r < red of A[i, r] 
     LinearEpilogue epi;
     float* part;             // fp32 [split, M, ldpart] when split > 1
     int ldpart, split, cfg, tiles_m, tiles_n;
+    int whole;               // tiles computed whole; the rest in quarters (256 x 256 tiles)
 };
 
 struct LinearDz {

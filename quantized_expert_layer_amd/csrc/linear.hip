@@ -13,24 +13,17 @@ namespace moe {
 // landed, and this stage's buffer, its second half read by then, takes the stage after the next.
 // ------------------------------------------------------------------------------------
 template <int DT, bool ACOLS, bool BCOLS, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearProduct p) {
+__device__ __forceinline__ void tile_body(const LinearProduct& p, char* lds, int z, int m0, int n0) {
 #ifdef __HIP_DEVICE_COMPILE__                  // the host pass has no buffer resources
     constexpr int W = WM * WN;
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;        // 16x16 subtiles per wave
     using OA = Operand<BM, ACOLS, W>;
     using OB = Operand<BN, BCOLS, W>;
     constexpr int kStage = OA::kBytes + OB::kBytes;
-    __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
 
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave / WN, wn = wave % WN;
-
-    const int tiles = p.tiles_m * p.tiles_n;
-    const int z = blockIdx.x / tiles;                          // split of the summed index
-    int tm, tn;
-    tile_of(p, blockIdx.x - z * tiles, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
 
     OA oa;
     OB ob;
@@ -144,28 +137,50 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearProduct
     // The accumulators (lane: row lane & 15 of a subtile, columns 4 (lane >> 4) .. + 3) leave
     // through the wave's own piece of LDS, two subtile rows at a time, so that a row's stores are
     // whole cache lines and the epilogue's code stands once.
-    constexpr int LPR = TN * 4, RPI = kWave / LPR;             // lanes per row, rows at a time
+    constexpr int LPR = TN * 2, RPI = kWave / LPR;             // lanes per row, rows at a time
+    constexpr int R = 32 / RPI, RB = R < 2 ? R : 2;            // a lane's rows, as many at once
     constexpr int RS = TN * 16 + 4;                            // fp32 row stride, padded
-    static_assert(W * 32 * RS * 4 <= (int)sizeof(lds) && TM % 2 == 0, "epilogue staging");
+    static_assert(W * 32 * RS * 4 <= 2 * kStage && TM % 2 == 0, "epilogue staging");
     __syncthreads();
     float* region = (float*)lds + wave * 32 * RS;
-    const int lr = lane / LPR, lc = (lane % LPR) * 4;
+    const int lr = lane / LPR, lc = (lane % LPR) * 8;
     const int col = n0 + wn * TN * 16 + lc;
-#pragma unroll
+    float bias[8];
+    load_bias<DT>(p.epi, col, p.N, bias);
     for (int h = 0; h < TM; h += 2) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < TM; ++i)
+            if (i - h == 0 || i - h == 1)
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
-                *(f32x4*)(region + (i * 16 + (lane & 15)) * RS + j * 16 + 4 * (lane >> 4)) = acc[h + i][j];
+                for (int j = 0; j < TN; ++j)
+                    *(f32x4*)(region + ((i & 1) * 16 + (lane & 15)) * RS + j * 16 + 4 * (lane >> 4)) =
+                        acc[i][j];
         lds_wave_fence();
-        const int row0 = m0 + (wm * TM + h) * 16 + lr;
-        for (int r = 0; r < 32; r += RPI) {
-            const int row = row0 + r;
-            if (row < p.M && col < p.N) {
-                const f32x4 v = *(const f32x4*)(region + (r + lr) * RS + lc);
-                if (p.part) *(f32x4*)(p.part + ((int64_t)z * p.M + row) * p.ldpart + col) = v;
-                else linear_epilogue4<DT>(p.epi, v, row, col, p.N);
+        for (int r0 = 0; r0 < R; r0 += RB) {
+            float v[RB][8];
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                const float* src = region + ((r0 + r) * RPI + lr) * RS + lc;
+                const f32x4 lo = *(const f32x4*)src, hi = *(const f32x4*)(src + 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[r][i] = lo[i];
+                    v[r][i + 4] = hi[i];
+                }
+            }
+            const int row0 = m0 + (wm * TM + h) * 16 + r0 * RPI + lr;
+            if (p.part) {                                      // their rows hold ldpart columns
+#pragma unroll
+                for (int r = 0; r < RB; ++r) {
+                    const int row = row0 + r * RPI;
+                    if (row < p.M && col < p.N) {
+                        float* dst = p.part + ((int64_t)z * p.M + row) * p.ldpart + col;
+                        *(f32x4*)dst = f32x4{v[r][0], v[r][1], v[r][2], v[r][3]};
+                        *(f32x4*)(dst + 4) = f32x4{v[r][4], v[r][5], v[r][6], v[r][7]};
+                    }
+                }
+            } else {
+                linear_epilogue<DT, RB>(p.epi, v, bias, row0, RPI, p.M, col, p.N);
             }
         }
         lds_wave_fence();
@@ -173,18 +188,51 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearProduct
 #endif
 }
 
+template <int DT, bool ACOLS, bool BCOLS, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearProduct p) {
+    __shared__ __attribute__((aligned(1024))) char lds[(BM + BN) * kBK * 2 * 2];
+    const int tiles = p.tiles_m * p.tiles_n;
+    int tm, tn;
+    if constexpr (BM == 256) {
+        const int b = blockIdx.x;
+        if (b >= p.whole) {                                    // a quarter of one of the last tiles
+            const int q = b - p.whole;
+            tile_at(p, p.whole + q / 4, tm, tn);
+            const int m0 = tm * BM + (q & 1) * (BM / 2), n0 = tn * BN + (q >> 1 & 1) * (BN / 2);
+            if (m0 < p.M && n0 < p.N)
+                tile_body<DT, ACOLS, BCOLS, BM / 2, BN / 2, WM, WN>(p, lds, 0, m0, n0);
+            return;
+        }
+    }
+    const int z = blockIdx.x / tiles;                          // split of the summed index
+    tile_of(p, blockIdx.x - z * tiles, BM == 256 && p.split == 1 ? p.whole : tiles, tm, tn);
+    tile_body<DT, ACOLS, BCOLS, BM, BN, WM, WN>(p, lds, z, tm * BM, tn * BN);
+}
+
 // Sums the splits' partial products in their order and applies the epilogue.
 template <int DT>
 __global__ __launch_bounds__(256) void linear_reduce_kernel(LinearProduct p) {
-    const int n4 = (p.N + 3) / 4;
-    const int64_t total = (int64_t)p.M * n4;
+    const int n8 = p.ldpart / 8;
+    const int64_t total = (int64_t)p.M * n8;
     for (int64_t i = blockIdx.x * 256 + (int64_t)threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / n4;
-        const int col = (int)(i - row * n4) * 4;
+        const int64_t row = i / n8;
+        const int col = (int)(i - row * n8) * 8;
         const float* src = p.part + row * p.ldpart + col;
-        f32x4 v = *(const f32x4*)src;
-        for (int z = 1; z < p.split; ++z) v += *(const f32x4*)(src + (int64_t)z * p.M * p.ldpart);
-        linear_epilogue4<DT>(p.epi, v, row, col, p.N);
+        f32x4 lo = *(const f32x4*)src, hi = *(const f32x4*)(src + 4);
+#pragma unroll 4
+        for (int z = 1; z < p.split; ++z) {
+            const float* sz = src + (int64_t)z * p.M * p.ldpart;
+            lo += *(const f32x4*)sz;
+            hi += *(const f32x4*)(sz + 4);
+        }
+        float v[1][8], bias[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            v[0][c] = lo[c];
+            v[0][c + 4] = hi[c];
+        }
+        load_bias<DT>(p.epi, col, p.N, bias);
+        linear_epilogue<DT, 1>(p.epi, v, bias, row, 0, p.M, col, p.N);
     }
 }
 
@@ -265,7 +313,8 @@ int grid_for(int64_t items, int per_block) {
 
 template <int DT, bool AC, bool BC>
 void launch_tiles(const LinearProduct& p, int cfg, hipStream_t s) {
-    const dim3 grid(p.tiles_m * p.tiles_n * p.split);
+    const int tiles = p.tiles_m * p.tiles_n;
+    const dim3 grid(cfg == 0 && p.split == 1 ? p.whole + 4 * (tiles - p.whole) : tiles * p.split);
     if (cfg == 0) linear_tile_kernel<DT, AC, BC, 256, 256, 2, 4><<<grid, 512, 0, s>>>(p);
     else if (cfg == 1) linear_tile_kernel<DT, AC, BC, 128, 128, 2, 2><<<grid, 256, 0, s>>>(p);
     else linear_tile_kernel<DT, AC, BC, 64, 64, 2, 2><<<grid, 256, 0, s>>>(p);
@@ -287,7 +336,14 @@ void linear_plan(LinearProduct& p) {
     p.split = split;
     p.tiles_m = (p.M + bm[cfg] - 1) / bm[cfg];
     p.tiles_n = (p.N + bm[cfg] - 1) / bm[cfg];
-    p.ldpart = (p.N + 3) / 4 * 4;
+    p.ldpart = (p.N + 7) / 8 * 8;
+    p.whole = p.tiles_m * p.tiles_n;
+    if (cfg == 0 && split == 1) {
+        const int last = p.whole % 256;
+        if (p.whole > 256 && last <= 128) p.whole -= last;
+    } else {
+        p.whole = p.tiles_m * p.tiles_n * split;
+    }
 }
 
 size_t linear_part_bytes(const LinearProduct& p) {
@@ -301,7 +357,7 @@ hipError_t launch_linear_product(const LinearProduct& p, int dtype, hipStream_t 
         else if (!p.a_cols) launch_tiles<DT, false, true>(p, p.cfg, s);
         else launch_tiles<DT, true, true>(p, p.cfg, s);
         if (p.split > 1)
-            linear_reduce_kernel<DT><<<grid_for((int64_t)p.M * ((p.N + 3) / 4), 256), 256, 0, s>>>(p);
+            linear_reduce_kernel<DT><<<grid_for((int64_t)p.M * (p.ldpart / 8), 256), 256, 0, s>>>(p);
     };
     if (dtype == MOE_DT_BF16) go(std::integral_constant<int, MOE_DT_BF16>{});
     else go(std::integral_constant<int, MOE_DT_FP16>{});

@@ -44,13 +44,11 @@ template <int DT> __device__ __forceinline__ uint16_t f32_to_dt(float v) {   // 
 // Activations on the fp32 sum and their slopes on the stored argument.  A NaN stays a NaN
 // (a maximum with 0 would drop it).
 __device__ __forceinline__ float gauss_cdf(float z) { return 0.5f * (1.0f + erff(z * 0.70710678f)); }
-__device__ __forceinline__ float act_value(float z, int act) {
-    switch (act) {
-        case MOE_ACT_RELU: return z < 0.0f ? 0.0f : z;
-        case MOE_ACT_SILU: return z / (1.0f + __expf(-z));
-        case MOE_ACT_GELU: return z * gauss_cdf(z);
-        default: return z;
-    }
+template <int ACT> __device__ __forceinline__ float act_value(float z) {
+    if constexpr (ACT == MOE_ACT_RELU) return z < 0.0f ? 0.0f : z;
+    else if constexpr (ACT == MOE_ACT_SILU) return z / (1.0f + __expf(-z));
+    else if constexpr (ACT == MOE_ACT_GELU) return z * gauss_cdf(z);
+    else return z;
 }
 __device__ __forceinline__ float act_slope(float z, int act) {
     switch (act) {
@@ -66,18 +64,20 @@ __device__ __forceinline__ float act_slope(float z, int act) {
 
 constexpr int kBK = 64;                         // summed indices per stage: a 128-byte line of a row
 
-// Tile of a block's index within one split.  Hardware block b runs on XCD b % 8, each with its own
-// L2: the tiles are cut into 8 contiguous ranges, one per XCD, and within a range run through
-// bands of 8 tile rows column by column, so that the tiles in flight on an XCD share operand rows.
-__device__ __forceinline__ void tile_of(const LinearProduct& p, int b, int& tm, int& tn) {
-    const int tiles = p.tiles_m * p.tiles_n;
-    const int q = tiles / 8, rem = tiles % 8, x = b % 8, i = b / 8;
-    const int t = x * q + min(x, rem) + i;
+// Tile t in the order the blocks take them: bands of 8 tile rows, column by column, so that the
+// tiles in flight share operand rows.
+__device__ __forceinline__ void tile_at(const LinearProduct& p, int t, int& tm, int& tn) {
     const int band = t / (8 * p.tiles_n);
     const int high = min(8, p.tiles_m - band * 8);
     const int in = t - band * 8 * p.tiles_n;
     tn = in / high;
     tm = band * 8 + in % high;
+}
+// Tile of block b of `tiles`.  Hardware block b runs on XCD b % 8, each with its own L2: the tiles
+// are cut into 8 contiguous ranges, one per XCD.
+__device__ __forceinline__ void tile_of(const LinearProduct& p, int b, int tiles, int& tm, int& tn) {
+    const int q = tiles / 8, rem = tiles % 8, x = b % 8;
+    tile_at(p, x * q + min(x, rem) + b / 8, tm, tn);
 }
 
 // Address past every buffer resource: such a lane's load delivers zeros.
@@ -191,56 +191,112 @@ struct Operand {
     };
 };
 
-// The linear layer's epilogue on four consecutive columns of one row.
+// ------------------------------------------------------------------------------------
+// The linear layer's epilogue on R rows x 8 consecutive columns per lane: row i of the lane is
+// row0 + i * step.  Uniform flags are tested once for all of the lane's values, and all residual
+// loads are issued before the first is used.
+// ------------------------------------------------------------------------------------
 template <int DT>
-__device__ __forceinline__ void linear_epilogue4(const LinearEpilogue& e, f32x4 v, int64_t row,
-                                                 int col, int n) {
-    const int live = min(4, n - col);                   // >= 1
+__device__ __forceinline__ void add16(float (&v)[8], const u32x4& r) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        v[2 * h] += dt_to_f32<DT>((uint16_t)r[h]);
+        v[2 * h + 1] += dt_to_f32<DT>((uint16_t)(r[h] >> 16));
+    }
+}
+template <int DT>
+__device__ __forceinline__ u32x4 pack16(const float (&v)[8]) {
+    u32x4 o;
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+        o[h] = f32_to_dt<DT>(v[2 * h]) | (uint32_t)f32_to_dt<DT>(v[2 * h + 1]) << 16;
+    return o;
+}
+template <int DT>
+__device__ __forceinline__ void load_bias(const LinearEpilogue& e, int col, int n, float (&b)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = (e.bias && col + i < n) ? dt_to_f32<DT>(e.bias[col + i]) : 0.0f;
+}
+template <int ACT, int R>
+__device__ __forceinline__ void apply_act(float (&v)[R][8]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[r][i] = act_value<ACT>(v[r][i]);
+}
+
+template <int DT, int R>
+__device__ __forceinline__ void linear_epilogue(const LinearEpilogue& e, float (&v)[R][8],
+                                                const float (&bias)[8], int64_t row0, int step,
+                                                int m, int col, int n) {
+    const int live = min(8, n - col);                   // columns of this lane, may be <= 0
+    const bool vec = live == 8 && e.vec;                // rows of 16-byte pieces throughout
+    bool ok[R];
+    u32x4 res[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        ok[r] = row0 + r * step < m && live > 0;
+        if (e.residual && vec && ok[r])
+            res[r] = *(const u32x4*)(e.residual + (row0 + r * step) * e.ldr + col);
+    }
     if (e.bias) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < live) v[i] += dt_to_f32<DT>(e.bias[col + i]);
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[r][i] += bias[i];
     }
     if (e.preact) {
-        uint16_t* dst = e.preact + row * e.ldp + col;
-        if (live == 4 && e.vec_pre) {
-            uint2 o;
-            o.x = f32_to_dt<DT>(v[0]) | (uint32_t)f32_to_dt<DT>(v[1]) << 16;
-            o.y = f32_to_dt<DT>(v[2]) | (uint32_t)f32_to_dt<DT>(v[3]) << 16;
-            *(uint2*)dst = o;
-        } else {
-            for (int i = 0; i < live; ++i) dst[i] = f32_to_dt<DT>(v[i]);
-        }
-    }
-    if (e.act != MOE_ACT_NONE) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = act_value(v[i], e.act);
-    }
-    if (e.residual) {
-        const uint16_t* src = e.residual + row * e.ldr + col;
-        if (live == 4 && e.vec_res) {
-            const uint2 r = *(const uint2*)src;
-            v[0] += dt_to_f32<DT>((uint16_t)r.x);
-            v[1] += dt_to_f32<DT>((uint16_t)(r.x >> 16));
-            v[2] += dt_to_f32<DT>((uint16_t)r.y);
-            v[3] += dt_to_f32<DT>((uint16_t)(r.y >> 16));
-        } else {
-            for (int i = 0; i < live; ++i) v[i] += dt_to_f32<DT>(src[i]);
+        for (int r = 0; r < R; ++r) {
+            if (!ok[r]) continue;
+            uint16_t* dst = e.preact + (row0 + r * step) * e.ldp + col;
+            if (vec) {
+                *(u32x4*)dst = pack16<DT>(v[r]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < live) dst[i] = f32_to_dt<DT>(v[r][i]);
+            }
         }
     }
-    if (e.out_f32) {
-        float* dst = (float*)e.out + row * e.ldo + col;
-        if (live == 4 && e.vec_out) *(f32x4*)dst = v;
-        else for (int i = 0; i < live; ++i) dst[i] = v[i];
-    } else {
-        uint16_t* dst = (uint16_t*)e.out + row * e.ldo + col;
-        if (live == 4 && e.vec_out) {
-            uint2 o;
-            o.x = f32_to_dt<DT>(v[0]) | (uint32_t)f32_to_dt<DT>(v[1]) << 16;
-            o.y = f32_to_dt<DT>(v[2]) | (uint32_t)f32_to_dt<DT>(v[3]) << 16;
-            *(uint2*)dst = o;
+    if (e.act == MOE_ACT_RELU) apply_act<MOE_ACT_RELU>(v);
+    else if (e.act == MOE_ACT_SILU) apply_act<MOE_ACT_SILU>(v);
+    else if (e.act == MOE_ACT_GELU) apply_act<MOE_ACT_GELU>(v);
+    if (e.residual) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (vec) {
+                if (ok[r]) add16<DT>(v[r], res[r]);
+            } else if (ok[r]) {
+                const uint16_t* src = e.residual + (row0 + r * step) * e.ldr + col;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < live) v[r][i] += dt_to_f32<DT>(src[i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (!ok[r]) continue;
+        if (e.out_f32) {
+            float* dst = (float*)e.out + (row0 + r * step) * e.ldo + col;
+            if (vec) {
+                *(f32x4*)dst = f32x4{v[r][0], v[r][1], v[r][2], v[r][3]};
+                *(f32x4*)(dst + 4) = f32x4{v[r][4], v[r][5], v[r][6], v[r][7]};
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < live) dst[i] = v[r][i];
+            }
         } else {
-            for (int i = 0; i < live; ++i) dst[i] = f32_to_dt<DT>(v[i]);
+            uint16_t* dst = (uint16_t*)e.out + (row0 + r * step) * e.ldo + col;
+            if (vec) {
+                *(u32x4*)dst = pack16<DT>(v[r]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < live) dst[i] = f32_to_dt<DT>(v[r][i]);
+            }
         }
     }
 }
