@@ -130,7 +130,6 @@ size_t decode_workspace_layout(int T, int k, int E, int d, int inter, int wtype,
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream);
 
 // ---- dense linear layer and its gradients ----
-constexpr int kLinearMaxSplit = 16;
 
 struct LinearEpilogue {      // out = act(sum + bias) + residual; preact = sum + bias
     const uint16_t* bias;    // [N] or NULL

@@ -12,7 +12,7 @@ namespace moe {
 // LDS read.  The barrier therefore sits in the middle of a stage: behind it the next stage has
 // landed, and this stage's buffer, its second half read by then, takes the stage after the next.
 // ------------------------------------------------------------------------------------
-template <int DT, bool ACOLS, bool BCOLS, int BM, int BN, int WM, int WN>
+template <int DT, bool ACOLS, bool BCOLS, int BM, int BN, int WM, int WN, int NBUF>
 __device__ __forceinline__ void tile_body(const LinearProduct& p, char* lds, int z, int m0, int n0) {
 #ifdef __HIP_DEVICE_COMPILE__                  // the host pass has no buffer resources
     constexpr int W = WM * WN;
@@ -99,37 +99,41 @@ __device__ __forceinline__ void tile_body(const LinearProduct& p, char* lds, int
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    // Behind the barrier all loads issued before it, by any wave, have landed and all LDS reads
-    // have been served.
+    // Behind the barrier all but the last `keep` stages that any wave has begun to load have landed,
+    // and all LDS reads have been served.
+    auto wait_loads = [](auto keep) {
+        constexpr int n = decltype(keep)::value * NL;
+        static_assert(n < 64, "vmcnt");
+        __builtin_amdgcn_s_waitcnt(0x0070 | (n & 15) | (n >> 4) << 14);   // vmcnt(n) lgkmcnt(0)
+    };
     auto land = [&]() {
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(0x0070);                    // vmcnt(0) lgkmcnt(0)
+        wait_loads(std::integral_constant<int, NBUF - 2>{});
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
     if (s0 < s1) {
         s16x8 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
-        Stage st = next_stage();
+        Stage st;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) load(st, i, 0);
-        st = next_stage();
+        for (int b = 0; b < NBUF; ++b) {
+            st = next_stage();
 #pragma unroll
-        for (int i = 0; i < NL; ++i) load(st, i, 1);
-        static_assert(NL < 16, "vmcnt");
-        __builtin_amdgcn_s_waitcnt(0x0f70 | NL);               // the first stage
+            for (int i = 0; i < NL; ++i) load(st, i, b);
+        }
+        wait_loads(std::integral_constant<int, NBUF - 1>{});
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int f = 0; f < TM + TN; ++f) read(fa0, fb0, f, 0, 0);
-        for (int s = s0; s < s1; s += 2) {
-            half(fa0, fb0, fa1, fb1, 0, 1, false, st, 0);
-            st = next_stage();
-            land();
-            half(fa1, fb1, fa0, fb0, 1, 0, true, st, 0);
-            half(fa0, fb0, fa1, fb1, 1, 1, false, st, 0);
-            st = next_stage();
-            land();
-            half(fa1, fb1, fa0, fb0, 0, 0, true, st, 1);
+        for (int s = s0; s < s1; s += NBUF) {
+#pragma unroll
+            for (int b = 0; b < NBUF; ++b) {
+                half(fa0, fb0, fa1, fb1, b, 1, false, st, 0);
+                st = next_stage();
+                land();
+                half(fa1, fb1, fa0, fb0, (b + 1) % NBUF, 0, true, st, b);
+            }
         }
         __builtin_amdgcn_s_waitcnt(0x0070);                    // nothing may land in LDS any more
     }
@@ -140,7 +144,7 @@ __device__ __forceinline__ void tile_body(const LinearProduct& p, char* lds, int
     constexpr int LPR = TN * 2, RPI = kWave / LPR;             // lanes per row, rows at a time
     constexpr int R = 32 / RPI, RB = R < 2 ? R : 2;            // a lane's rows, as many at once
     constexpr int RS = TN * 16 + 4;                            // fp32 row stride, padded
-    static_assert(W * 32 * RS * 4 <= 2 * kStage && TM % 2 == 0, "epilogue staging");
+    static_assert(W * 32 * RS * 4 <= NBUF * kStage && TM % 2 == 0, "epilogue staging");
     __syncthreads();
     float* region = (float*)lds + wave * 32 * RS;
     const int lr = lane / LPR, lc = (lane % LPR) * 8;
@@ -188,25 +192,25 @@ __device__ __forceinline__ void tile_body(const LinearProduct& p, char* lds, int
 #endif
 }
 
-template <int DT, bool ACOLS, bool BCOLS, int BM, int BN, int WM, int WN>
+template <int DT, bool ACOLS, bool BCOLS, int BM, int BN, int WM, int WN, int NBUF>
 __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearProduct p) {
-    __shared__ __attribute__((aligned(1024))) char lds[(BM + BN) * kBK * 2 * 2];
+    __shared__ __attribute__((aligned(1024))) char lds[(BM + BN) * kBK * 2 * NBUF];
     const int tiles = p.tiles_m * p.tiles_n;
     int tm, tn;
     if constexpr (BM == 256) {
         const int b = blockIdx.x;
-        if (b >= p.whole) {                                    // a quarter of one of the last tiles
+        if (p.split == 1 && b >= p.whole) {                    // a quarter of one of the last tiles
             const int q = b - p.whole;
             tile_at(p, p.whole + q / 4, tm, tn);
             const int m0 = tm * BM + (q & 1) * (BM / 2), n0 = tn * BN + (q >> 1 & 1) * (BN / 2);
             if (m0 < p.M && n0 < p.N)
-                tile_body<DT, ACOLS, BCOLS, BM / 2, BN / 2, WM, WN>(p, lds, 0, m0, n0);
+                tile_body<DT, ACOLS, BCOLS, BM / 2, BN / 2, WM, WN, 4>(p, lds, 0, m0, n0);
             return;
         }
     }
     const int z = blockIdx.x / tiles;                          // split of the summed index
-    tile_of(p, blockIdx.x - z * tiles, BM == 256 && p.split == 1 ? p.whole : tiles, tm, tn);
-    tile_body<DT, ACOLS, BCOLS, BM, BN, WM, WN>(p, lds, z, tm * BM, tn * BN);
+    tile_of(p, blockIdx.x - z * tiles, p.split == 1 ? p.whole : tiles, tm, tn);
+    tile_body<DT, ACOLS, BCOLS, BM, BN, WM, WN, NBUF>(p, lds, z, tm * BM, tn * BN);
 }
 
 // Sums the splits' partial products in their order and applies the epilogue.
@@ -311,38 +315,79 @@ int grid_for(int64_t items, int per_block) {
     return (int)(want < 1 ? 1 : want > 16384 ? 16384 : want);
 }
 
+// The tiles, and what a block of each was measured to take (us): `base` outside the loop over the
+// stages (first loads, epilogue), `stage` per 64 summed indices, alone on its CU or with a second
+// block on it.  Larger tiles move fewer bytes per product, smaller ones fill the chip with less
+// work.  Four stages in LDS instead of two cover the memory's latency where the stage is short and
+// the block alone (128 x 128, 2048 x 2048 x 2048: 20.0 against 24.8 us); two blocks of two stages
+// do it as well where there are tiles enough (2048 x 4096 x 4096: 65 against 70 us).
+struct TileCost {
+    int bm, bn, buffers, per_cu;
+    double base, stage, base2, stage2;
+};
+constexpr TileCost kTiles[] = {
+    {256, 256, 2, 1, 7.0, 1.15, 0.0, 0.0},
+    {128, 128, 4, 1, 2.5, 0.50, 0.0, 0.0},
+    {128, 128, 2, 2, 3.0, 0.60, 3.5, 0.92},
+    {64, 128, 4, 1, 1.5, 0.34, 0.0, 0.0},
+    {64, 64, 4, 2, 1.0, 0.245, 1.3, 0.38},
+};
+constexpr int kCus = 256;
+
 template <int DT, bool AC, bool BC>
-void launch_tiles(const LinearProduct& p, int cfg, hipStream_t s) {
+void launch_tiles(const LinearProduct& p, hipStream_t s) {
     const int tiles = p.tiles_m * p.tiles_n;
-    const dim3 grid(cfg == 0 && p.split == 1 ? p.whole + 4 * (tiles - p.whole) : tiles * p.split);
-    if (cfg == 0) linear_tile_kernel<DT, AC, BC, 256, 256, 2, 4><<<grid, 512, 0, s>>>(p);
-    else if (cfg == 1) linear_tile_kernel<DT, AC, BC, 128, 128, 2, 2><<<grid, 256, 0, s>>>(p);
-    else linear_tile_kernel<DT, AC, BC, 64, 64, 2, 2><<<grid, 256, 0, s>>>(p);
+    const dim3 grid(p.split > 1 ? tiles * p.split : p.whole + 4 * (tiles - p.whole));
+    switch (p.cfg) {
+        case 0: linear_tile_kernel<DT, AC, BC, 256, 256, 2, 4, 2><<<grid, 512, 0, s>>>(p); break;
+        case 1: linear_tile_kernel<DT, AC, BC, 128, 128, 2, 4, 4><<<grid, 512, 0, s>>>(p); break;
+        case 2: linear_tile_kernel<DT, AC, BC, 128, 128, 2, 4, 2><<<grid, 512, 0, s>>>(p); break;
+        case 3: linear_tile_kernel<DT, AC, BC, 64, 128, 2, 4, 4><<<grid, 512, 0, s>>>(p); break;
+        default: linear_tile_kernel<DT, AC, BC, 64, 64, 2, 2, 4><<<grid, 256, 0, s>>>(p); break;
+    }
 }
 
 }  // namespace
 
 void linear_plan(LinearProduct& p) {
-    static const int bm[3] = {256, 128, 64};
     const int stages = ((p.red + kBK - 1) / kBK) * p.parts;
-    auto tiles = [&](int c) {
-        return (int64_t)((p.M + bm[c] - 1) / bm[c]) * ((p.N + bm[c] - 1) / bm[c]);
-    };
-    int cfg = 0;
-    while (cfg < 2 && tiles(cfg) < 200) ++cfg;
-    int split = 1;
-    while (split < kLinearMaxSplit && tiles(cfg) * (split + 1) <= 320 && stages / (split + 1) >= 8) ++split;
-    p.cfg = cfg;
-    p.split = split;
-    p.tiles_m = (p.M + bm[cfg] - 1) / bm[cfg];
-    p.tiles_n = (p.N + bm[cfg] - 1) / bm[cfg];
     p.ldpart = (p.N + 7) / 8 * 8;
-    p.whole = p.tiles_m * p.tiles_n;
-    if (cfg == 0 && split == 1) {
-        const int last = p.whole % 256;
-        if (p.whole > 256 && last <= 128) p.whole -= last;
-    } else {
-        p.whole = p.tiles_m * p.tiles_n * split;
+    double best = 1e30;
+    for (int c = 0; c < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++c) {
+        const TileCost& t = kTiles[c];
+        const int tm = (p.M + t.bm - 1) / t.bm, tn = (p.N + t.bn - 1) / t.bn;
+        for (int split : {1, 2, 3, 4, 6, 8, 12, 16}) {
+            if (split > 1 && stages < 2 * split) break;
+            int64_t blocks = (int64_t)tm * tn * split;
+            if (split > 1 && blocks > 4 * kCus) break;
+            const int st = ((stages + split - 1) / split + t.buffers - 1) / t.buffers * t.buffers;
+            // rounds of one block, or two, per CU; a split's sums are written and read once more
+            // by a launch of their own (4.4 TB/s)
+            double us = split > 1 ? 4.5 + 8.0 * split * p.M * (double)p.ldpart / 4.4e6 : 0.0;
+            int64_t whole = blocks;
+            const int64_t last = blocks % kCus;
+            if (c == 0 && split == 1 && blocks > kCus && last <= kCus / 2) {
+                whole -= last;                     // the last round in quarters
+                us += (double)((4 * last + kCus - 1) / kCus) * (2.5 + 0.55 * st);
+            }
+            if (t.per_cu == 2) {
+                us += (double)(whole / (2 * kCus)) * (t.base2 + t.stage2 * st);
+                whole %= 2 * kCus;
+                if (whole > kCus) {
+                    us += t.base2 + t.stage2 * st;
+                    whole = 0;
+                }
+            }
+            us += (double)((whole + kCus - 1) / kCus) * (t.base + t.stage * st);
+            if (us < best) {
+                best = us;
+                p.cfg = c;
+                p.split = split;
+                p.tiles_m = tm;
+                p.tiles_n = tn;
+                p.whole = tm * tn - (int)(c == 0 && split == 1 && blocks > kCus && last <= kCus / 2 ? last : 0);
+            }
+        }
     }
 }
 
@@ -353,9 +398,9 @@ size_t linear_part_bytes(const LinearProduct& p) {
 hipError_t launch_linear_product(const LinearProduct& p, int dtype, hipStream_t s) {
     auto go = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        if (!p.a_cols && !p.b_cols) launch_tiles<DT, false, false>(p, p.cfg, s);
-        else if (!p.a_cols) launch_tiles<DT, false, true>(p, p.cfg, s);
-        else launch_tiles<DT, true, true>(p, p.cfg, s);
+        if (!p.a_cols && !p.b_cols) launch_tiles<DT, false, false>(p, s);
+        else if (!p.a_cols) launch_tiles<DT, false, true>(p, s);
+        else launch_tiles<DT, true, true>(p, s);
         if (p.split > 1)
             linear_reduce_kernel<DT><<<grid_for((int64_t)p.M * (p.ldpart / 8), 256), 256, 0, s>>>(p);
     };
