@@ -674,7 +674,7 @@ LinearBackward linear_backward(int32_t M, int32_t N, int32_t K, int64_t lda, int
     f.dz.parts = parts;
     const int64_t ldz = f.need_dz ? N8 : ldg;
     if (f.need_dz) f.dz.dz = (uint16_t*)c.take((size_t)parts * M * N8 * 2);
-    f.dz.sums = (float*)c.take((size_t)moe::linear_dz_blocks(M) * N * 4);
+    f.dz.sums = (float*)c.take((size_t)moe::linear_dz_blocks(M, N) * N * 4);
     if (!in_pieces(K, ldw)) {
         f.pack_w = (uint16_t*)c.take((size_t)N * K8 * 2);
         ldw = K8;
@@ -826,6 +826,7 @@ int32_t moe_linear_backward(const void* grad_out, int64_t ldg, int32_t grad_dtyp
         z.preact = preact;
         z.ldp = ldp;
         z.act = act;
+        z.vec = ldg % 8 == 0 && (act == MOE_ACT_NONE || ldp % 8 == 0);
         z.M = M;
         z.N = N;
         if (!grad_a && !grad_w) z.dz = nullptr;

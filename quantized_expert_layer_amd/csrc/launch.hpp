@@ -167,7 +167,9 @@ struct LinearDz {
     int act, M, N, cols8;
     uint16_t* dz;            // [parts, M, cols8] or NULL
     int parts;
-    float* sums;             // [linear_dz_blocks(M), N] or NULL
+    float* sums;             // [linear_dz_blocks(M, N), N] or NULL
+    int vec;                 // rows of grad and preact start on 16 bytes
+    int lc;                  // log2 of a block's threads across the columns (set by the launch)
 };
 
 // Chooses tile, split and the partial layout from the sizes (host-only, deterministic).
@@ -176,7 +178,7 @@ size_t linear_part_bytes(const LinearProduct& p);
 hipError_t launch_linear_product(const LinearProduct& p, int dtype, hipStream_t stream);
 hipError_t launch_linear_pack(const uint16_t* src, int64_t ld, int rows, int cols, uint16_t* dst,
                               hipStream_t stream);
-int linear_dz_blocks(int M);
+int linear_dz_blocks(int M, int N);
 hipError_t launch_linear_dz(const LinearDz& p, int dtype, uint16_t* grad_bias, hipStream_t stream);
 
 // ---- balance loss and the router's gradients ----

@@ -43,22 +43,49 @@ template <int DT> __device__ __forceinline__ uint16_t f32_to_dt(float v) {   // 
 
 // Activations on the fp32 sum and their slopes on the stored argument.  A NaN stays a NaN
 // (a maximum with 0 would drop it).
-__device__ __forceinline__ float gauss_cdf(float z) { return 0.5f * (1.0f + erff(z * 0.70710678f)); }
+//
+// The normal distribution function from erfc(x) = e^(-x^2) P(t), t = 1 / (1 + 0.42 x), x = |z| / sqrt 2:
+// P is a least-maximum fit of e^(x^2) erfc(x) in t over 0 <= x <= 9.6 (beyond, e^(-x^2) is 0 in
+// fp32), relative error 4e-8; in fp32 the result is within 2.3e-7, and within 2.2e-6 of itself in
+// the lower tail.  Half the instructions of erff, which at 8192 x 6400 outputs cost 60 us of
+// arithmetic between the products.
+__device__ __forceinline__ float gauss_cdf(float z, float& bell) {       // bell = e^(-z^2 / 2)
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.29698485f * fabsf(z));
+    float h = 0.078389115f;
+    h = h * t - 0.35694963f;
+    h = h * t + 0.51032633f;
+    h = h * t - 0.20320329f;
+    h = h * t + 0.31420779f;
+    h = h * t + 0.17730533f;
+    h = h * t + 0.24357177f;
+    h = h * t + 0.23632675f;
+    h = h * t + 2.5940517e-5f;
+    bell = __expf(-0.5f * z * z);
+    const float q = 0.5f * h * bell;
+    return z < 0.0f ? q : 1.0f - q;
+}
+__device__ __forceinline__ float sigmoid(float z) {
+    return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
 template <int ACT> __device__ __forceinline__ float act_value(float z) {
+    float bell;
     if constexpr (ACT == MOE_ACT_RELU) return z < 0.0f ? 0.0f : z;
-    else if constexpr (ACT == MOE_ACT_SILU) return z / (1.0f + __expf(-z));
-    else if constexpr (ACT == MOE_ACT_GELU) return z * gauss_cdf(z);
+    else if constexpr (ACT == MOE_ACT_SILU) return z * sigmoid(z);
+    else if constexpr (ACT == MOE_ACT_GELU) return z * gauss_cdf(z, bell);
     else return z;
 }
-__device__ __forceinline__ float act_slope(float z, int act) {
-    switch (act) {
-        case MOE_ACT_RELU: return z <= 0.0f ? 0.0f : 1.0f;
-        case MOE_ACT_SILU: {
-            const float s = 1.0f / (1.0f + __expf(-z));
-            return s * (1.0f + z * (1.0f - s));
-        }
-        case MOE_ACT_GELU: return gauss_cdf(z) + z * 0.39894228f * __expf(-0.5f * z * z);
-        default: return 1.0f;
+template <int ACT> __device__ __forceinline__ float act_slope(float z) {
+    if constexpr (ACT == MOE_ACT_RELU) {
+        return z <= 0.0f ? 0.0f : 1.0f;
+    } else if constexpr (ACT == MOE_ACT_SILU) {
+        const float s = sigmoid(z);
+        return s * (1.0f + z * (1.0f - s));
+    } else if constexpr (ACT == MOE_ACT_GELU) {
+        float bell;
+        const float c = gauss_cdf(z, bell);
+        return c + z * 0.39894228f * bell;
+    } else {
+        return 1.0f;
     }
 }
 

@@ -214,18 +214,14 @@ __global__ __launch_bounds__(1024) void balance_segment_kernel(BalanceParams p) 
 // Gradient of the logits, one token per 16-lane row.
 template <int PER_LANE>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradParams p) {
-    __shared__ int used_waves[4];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int j16 = lane & 15, row = lane >> 4;
     int used = 1;
     if (p.counts && p.S > 1) {                     // segments with tokens
         used = 0;
-        for (int i = threadIdx.x; i < p.S; i += 256) used += p.tokens[i] > 0;
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) used += __shfl_xor(used, o);
-        if (lane == 0) used_waves[wave] = used;
-        __syncthreads();
-        used = max(used_waves[0] + used_waves[1] + used_waves[2] + used_waves[3], 1);
+        for (int i = 0; i < p.S; i += kWave)
+            used += __popcll(__ballot(i + lane < p.S && p.tokens[i + lane] > 0));
+        used = max(used, 1);
     }
     const float scale = p.counts ? p.coef * (p.grad_loss ? *p.grad_loss : 1.0f) / (float)used : 0.0f;
     const int t = (blockIdx.x * 4 + wave) * 4 + row;
