@@ -199,6 +199,7 @@ struct BalanceParams {
     int32_t* part_counts;    // [pieces, E]
     int32_t* part_tokens;    // [pieces]
     float* terms;            // [S]
+    int vec;                 // rows of logits in 16-byte pieces (set by the launch)
 };
 size_t balance_workspace_layout(int T, int E, int S, BalanceParams* p, char* base);
 hipError_t launch_balance(const BalanceParams& p, hipStream_t stream);
@@ -216,6 +217,7 @@ struct RouteGradParams {
     float coef;
     const float* grad_loss;  // or NULL: 1
     float* grad;
+    int vec;                 // rows in 16-byte pieces (set by the launch)
 };
 hipError_t launch_route_backward(const RouteGradParams& p, hipStream_t stream);
 

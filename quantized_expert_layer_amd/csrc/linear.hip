@@ -240,6 +240,84 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(LinearProduct p) {
     }
 }
 
+// ------------------------------------------------------------------------------------
+// Few rows (M <= 32, decode and verify steps): out = a w^T is one pass over the weights.  A block
+// takes 16 weight rows, its waves an even share of K each, straight from memory to registers, four
+// stages (8 KB of weights a wave) in flight; the waves' sums meet in LDS in wave order, where the
+// epilogue runs, so the product is one launch without a workspace.  Bound by the weights' read and
+// its latency: 1 x 4096 x 4096 bf16, 34 MB, 8.8 us (6.5 us at a copy's rate).  Six stages in flight in
+// a ring took longer (12.2 us): a wave's share is four stages or fewer here.
+// ------------------------------------------------------------------------------------
+template <int DT, int MT>
+__global__ __launch_bounds__(1024) void linear_stream_kernel(LinearProduct p) {
+#ifdef __HIP_DEVICE_COMPILE__
+    __shared__ f32x4 sums[16][MT][kWave];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), waves = blockDim.x / kWave;
+    const int n0 = blockIdx.x * 16;
+    const int stages = (p.red + kBK - 1) / kBK;
+    const int s0 = (int)((int64_t)stages * wave / waves), s1 = (int)((int64_t)stages * (wave + 1) / waves);
+    // rows past the matrices and summed indices past K read as zeros
+    const int ld_b = (int)p.ldb, ld_a = (int)p.lda;
+    const auto wb = buffer_of(p.b + (int64_t)n0 * ld_b,
+                              ((uint32_t)(min(16, p.b_outs - n0) - 1) * ld_b + p.red) * 2u);
+    const auto ab = buffer_of(p.a, ((uint32_t)(p.a_outs - 1) * ld_a + p.red) * 2u);
+    const int kl = 8 * (lane >> 4);
+    const uint32_t wo = (uint32_t)((lane & 15) * ld_b + kl) * 2u;
+    const uint32_t ao = (uint32_t)((lane & 15) * ld_a + kl) * 2u;
+    const bool w_row = n0 + (lane & 15) < p.b_outs;
+    // the epilogue's thread: row t / 2, eight columns
+    const int t = threadIdx.x, row = t / 2, c8 = (t & 1) * 8;
+    const int col = n0 + c8;
+    const bool out = row < p.M && row < 16 * MT && col < p.N;
+    float v[1][8] = {}, bias[8] = {};
+    if (out) load_bias<DT>(p.epi, col, p.N, bias);
+    f32x4 acc[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    constexpr int U = 4;                                       // stages in flight
+    for (int s = s0; s < s1; s += U) {
+        s16x8 w[U][2], a[U][2][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = (s + u) * kBK + 32 * h;
+                const bool in = s + u < s1 && k + kl < p.red;
+                w[u][h] = __builtin_bit_cast(s16x8, __builtin_amdgcn_raw_buffer_load_b128(
+                    wb, in && w_row ? wo + k * 2u : kOutside, 0, 0));
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                    a[u][h][m] = __builtin_bit_cast(s16x8, __builtin_amdgcn_raw_buffer_load_b128(
+                        ab, in && 16 * m + (lane & 15) < p.a_outs ? ao + (uint32_t)(16 * m * ld_a + k) * 2u
+                                                                  : kOutside, 0, 0));
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) acc[m] = mfma_dt<DT>(w[u][h], a[u][h][m], acc[m]);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) sums[wave][m][lane] = acc[m];
+    __syncthreads();
+    if (!out) return;
+    // eight columns sit in lanes row + 16 (column / 4)
+    const int at = (row & 15) + 16 * (c8 / 4);
+#pragma unroll 4
+    for (int i = 0; i < waves; ++i) {
+        const f32x4 lo = sums[i][row >> 4][at], hi = sums[i][row >> 4][at + 16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            v[0][c] += lo[c];
+            v[0][c + 4] += hi[c];
+        }
+    }
+    linear_epilogue<DT, 1>(p.epi, v, bias, row, 0, p.M, col, p.N);
+#endif
+}
+
 // Copies a 16-bit matrix whose rows cannot be read in 16-byte pieces (row length or stride not a
 // multiple of 8) into rows of cols8 = cols rounded up to 8, zeros behind.
 __global__ __launch_bounds__(256) void linear_pack_kernel(const uint16_t* __restrict__ src,
@@ -403,6 +481,22 @@ constexpr TileCost kTiles[] = {
     {64, 64, 4, 2, 1.0, 0.245, 1.3, 0.38},
 };
 constexpr int kCus = 256;
+// linear_stream_kernel instead of a tile, for products of up to 32 rows and kStreamMost terms.  On
+// the device (bf16, us, stream against tile): 1 x 4096 x 4096 8.8 / 12.0, 17 x 2048 x 2048 8.7 / 8.7,
+// 16 x 4096 x 4096 11.4 / 12.5, 16 x 4096 x 6400 20.0 / 15.6 -- and one launch less on the host.
+constexpr int kStream = 100;
+constexpr int64_t kStreamMost = (int64_t)1 << 28;
+
+// Waves per block: about 4096 in all, 4 to 16 a block, at most one per stage of K.
+template <int DT>
+void launch_stream(const LinearProduct& p, hipStream_t s) {
+    const int stages = (p.red + kBK - 1) / kBK, grid = (p.N + 15) / 16;
+    int waves = 4096 / grid;
+    waves = waves < 4 ? 4 : waves > 16 ? 16 : waves;
+    if (waves > stages) waves = stages;
+    if (p.M <= 16) linear_stream_kernel<DT, 1><<<grid, waves * kWave, 0, s>>>(p);
+    else linear_stream_kernel<DT, 2><<<grid, waves * kWave, 0, s>>>(p);
+}
 
 template <int DT, bool AC, bool BC>
 void launch_tiles(const LinearProduct& p, hipStream_t s) {
@@ -420,6 +514,11 @@ void launch_tiles(const LinearProduct& p, hipStream_t s) {
 }  // namespace
 
 void linear_plan(LinearProduct& p) {
+    if (!p.a_cols && !p.b_cols && p.M <= 32 && (int64_t)p.M * p.N * p.red <= kStreamMost) {
+        p.cfg = kStream;
+        p.split = 1;
+        return;
+    }
     const int stages = ((p.red + kBK - 1) / kBK) * p.parts;
     p.ldpart = (p.N + 7) / 8 * 8;
     double best = 1e30;
@@ -468,7 +567,8 @@ size_t linear_part_bytes(const LinearProduct& p) {
 hipError_t launch_linear_product(const LinearProduct& p, int dtype, hipStream_t s) {
     auto go = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
-        if (!p.a_cols && !p.b_cols) launch_tiles<DT, false, false>(p, s);
+        if (p.cfg == kStream) launch_stream<DT>(p, s);
+        else if (!p.a_cols && !p.b_cols) launch_tiles<DT, false, false>(p, s);
         else if (!p.a_cols) launch_tiles<DT, false, true>(p, s);
         else launch_tiles<DT, true, true>(p, s);
         if (p.split > 1)

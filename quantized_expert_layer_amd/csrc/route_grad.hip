@@ -1,8 +1,11 @@
 // The router's balance loss with its counts, the gradient of the router logits, and the gradients
 // of the combine (of the gate weights and of the expert rows).
 //
-// Softmax rows are held as in the gating: one token per 16-lane row of a wave, lane j of the row
-// with experts j, j + 16, ... (PER_LANE of them), so a row's maximum and sum are DPP reductions.
+// One token per 16-lane row of a wave, as in the gating, but lane j of the row holds the PER_LANE
+// consecutive experts from j PER_LANE on: a row's maximum and sum are DPP reductions, and its loads
+// and stores go in 16-byte pieces where E is a multiple of 4.
+#include <type_traits>
+
 #include "common.hpp"
 #include "launch.hpp"
 #include "route.hpp"
@@ -16,28 +19,60 @@ __device__ __forceinline__ float row_total(float v) {
     }));
 }
 
-// Probabilities of one token's experts: softmax over its E logits; -inf and NaN have none, and a
-// row with nothing else has none at all.
+// e^x for x <= 0: the product with log2 e is taken in two parts, so its rounding (|x| 2^-24 of the
+// result otherwise) is kept.  A third of expf's instructions, which bound these kernels.  Below
+// -120 the result is 0 (and the product of a masked logit's lowest value would overflow).
+__device__ __forceinline__ float exp_near(float x) {
+    x = x < -120.0f ? -120.0f : x;
+    const float hi = x * 1.44269504f, lo = fmaf(x, 1.44269504f, -hi);
+    const float e = __builtin_amdgcn_exp2f(hi);
+    return fmaf(e, lo * 0.69314718f, e);
+}
+// Lane j of each 16-lane row, in all lanes of the row.
+template <int J> __device__ __forceinline__ int row_lane(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, 0x150 + J, 0xF, 0xF, false);   // row_newbcast
+}
+
+// This lane's part of a row of E values (experts past E read as some other).  Rows without a live
+// token are loaded all the same, from a valid place: a load that waits for a flag costs a memory
+// latency.
+template <int PER_LANE, typename T>
+__device__ __forceinline__ void load_row(const T* row, int E, int j16, bool vec, T (&x)[PER_LANE]) {
+    if constexpr (PER_LANE >= 4) {
+        if (vec) {
+            typedef T T4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+            for (int i = 0; i < PER_LANE; i += 4) {
+                const T4 v = *(const T4*)(row + min(j16 * PER_LANE + i, E - 4));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x[i + c] = v[c];
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < PER_LANE; ++i) x[i] = row[min(j16 * PER_LANE + i, E - 1)];
+}
+// Probabilities of the token's experts: softmax over its E logits; -inf and NaN have none, and a
+// row with nothing else (or no live token) has none at all.
 template <int PER_LANE>
-__device__ __forceinline__ void softmax_row(const float* row, int E, int j16, float (&p)[PER_LANE]) {
+__device__ __forceinline__ void softmax_row(const float (&x)[PER_LANE], bool live, int E, int j16,
+                                            float (&p)[PER_LANE]) {
     float m = -__builtin_inff();
 #pragma unroll
     for (int i = 0; i < PER_LANE; ++i) {
-        const int e = j16 + 16 * i;
-        float x = (row && e < E) ? row[e] : -__builtin_inff();
-        if (x != x) x = -__builtin_inff();
-        p[i] = x;
-        m = fmaxf(m, x);
+        p[i] = (live && j16 * PER_LANE + i < E && x[i] == x[i]) ? x[i] : -__builtin_inff();
+        m = fmaxf(m, p[i]);
     }
     m = row_max_f32(m);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER_LANE; ++i) {
-        p[i] = p[i] == -__builtin_inff() ? 0.0f : expf(p[i] - m);
+        p[i] = p[i] == -__builtin_inff() ? 0.0f : exp_near(p[i] - m);
         sum += p[i];
     }
     sum = row_total(sum);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float inv = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
 #pragma unroll
     for (int i = 0; i < PER_LANE; ++i) p[i] *= inv;
 }
@@ -95,26 +130,39 @@ __global__ __launch_bounds__(256) void balance_piece_kernel(BalanceParams p) {
 #pragma unroll
     for (int i = 0; i < PER_LANE; ++i) acc[i] = 0.0f;
     int seen = 0;
-    for (int t0 = lo + wave * 4; t0 < hi; t0 += 16) {
-        const int t = t0 + row;
-        const bool live = t < hi && (!p.active || p.active[t]);
+    // the next 16 tokens' logits, ids and flags are on their way while these are summed
+    float x[PER_LANE], nx[PER_LANE];
+    int id = -1, nid = -1;
+    bool live = false, nlive = false;
+    auto fetch = [&](int t0, float (&v)[PER_LANE], int& vid, bool& vlive) {
+        const int t = t0 + row, tc = min(t, p.T - 1);
+        load_row<PER_LANE>(p.logits + (size_t)tc * p.E, p.E, j16, p.vec, v);
+        vid = p.ids[(size_t)tc * p.k + min(j16, p.k - 1)];
+        vlive = t < hi && (!p.active || p.active[tc]);
+    };
+    const int first = lo + wave * 4;
+    if (first < hi) fetch(first, x, id, live);
+    for (int t0 = first; t0 < hi; t0 += 16) {
+        const bool more = t0 + 16 < hi;                            // wave-uniform
+        if (more) fetch(t0 + 16, nx, nid, nlive);
         float pr[PER_LANE];
-        softmax_row<PER_LANE>(live ? p.logits + (size_t)t * p.E : nullptr, p.E, j16, pr);
+        softmax_row<PER_LANE>(x, live, p.E, j16, pr);
 #pragma unroll
         for (int i = 0; i < PER_LANE; ++i) acc[i] += pr[i];
         if (live) {
             seen += j16 == 0;
-            if (j16 < p.k) {
-                const int id = p.ids[(size_t)t * p.k + j16];
-                if ((unsigned)id < (unsigned)p.E) atomicAdd(&counts[id], 1);
-            }
+            if (j16 < p.k && (unsigned)id < (unsigned)p.E) atomicAdd(&counts[id], 1);
         }
+#pragma unroll
+        for (int i = 0; i < PER_LANE; ++i) x[i] = nx[i];
+        id = nid;
+        live = nlive;
     }
 #pragma unroll
     for (int i = 0; i < PER_LANE; ++i) {
         acc[i] += __shfl_xor(acc[i], 16);
         acc[i] += __shfl_xor(acc[i], 32);
-        if (row == 0) sums[wave][j16 + 16 * i] = acc[i];
+        if (row == 0) sums[wave][j16 * PER_LANE + i] = acc[i];
     }
     if (seen) atomicAdd(&live_tokens, seen);
     __syncthreads();
@@ -125,7 +173,7 @@ __global__ __launch_bounds__(256) void balance_piece_kernel(BalanceParams p) {
     if (threadIdx.x == 0) p.part_tokens[blockIdx.x] = live_tokens;
 }
 
-// Fixed-order sum over the block's 1024 threads (in thread 0).
+// Fixed-order sum over the block's threads (in thread 0).
 template <typename T>
 __device__ __forceinline__ T block_sum(T v, T* scratch) {
 #pragma unroll
@@ -135,7 +183,7 @@ __device__ __forceinline__ T block_sum(T v, T* scratch) {
     __syncthreads();
     T r = 0;
     if (threadIdx.x == 0)
-        for (int w = 0; w < 16; ++w) r += scratch[w];
+        for (int w = 0; w < (int)blockDim.x / 64; ++w) r += scratch[w];
     return r;
 }
 
@@ -146,33 +194,33 @@ __global__ __launch_bounds__(1024) void balance_segment_kernel(BalanceParams p) 
     __shared__ float fsum[1024];
     __shared__ int isum[1024];
     __shared__ float fs[16];
-    __shared__ int is[16], is2[16];
-    __shared__ int n_live, last;
-    const int s = blockIdx.x, tid = threadIdx.x;
+    __shared__ int is[16];
+    __shared__ int n_part[16], last;
+    const int s = blockIdx.x, tid = threadIdx.x, threads = blockDim.x;
     int first = 0, end = p.pieces;
     if (p.offsets) {
         const int lo = clamp_offset(p.offsets, s, p.T), hi = clamp_offset(p.offsets, s + 1, p.T);
         first = min(lo / p.cell + s, p.pieces);
         end = hi > lo ? min((hi - 1) / p.cell + s + 1, p.pieces) : first;
     }
-    int n = 0;
-    for (int b = first + tid; b < end; b += 1024) n += p.part_tokens[b];
-    n = block_sum(n, is);
-    if (tid == 0) n_live = n;
     const int ep = p.E <= 16 ? 16 : p.E <= 64 ? 64 : p.E <= 128 ? 128 : 256;
-    const int groups = 1024 / ep, g = tid / ep, e = tid % ep;
+    const int groups = threads / ep, g = tid / ep, e = tid % ep, ec = min(e, p.E - 1);
     float f = 0.0f;
-    int c = 0;
-    if (e < p.E) {
-        for (int b = first + g; b < end; b += groups) {
-            f += p.part_sums[(size_t)b * p.E + e];
-            c += p.part_counts[(size_t)b * p.E + e];
-        }
+    int c = 0, n = 0;
+#pragma unroll 8
+    for (int b = first + g; b < end; b += groups) {
+        f += p.part_sums[(size_t)b * p.E + ec];
+        c += p.part_counts[(size_t)b * p.E + ec];
     }
+    for (int b = first + tid; b < end; b += threads) n += p.part_tokens[b];
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o);
+    if ((tid & 63) == 0) n_part[tid / 64] = n;
     fsum[tid] = f;
     isum[tid] = c;
     __syncthreads();
-    n = n_live;
+    n = 0;
+    for (int w = 0; w < threads / 64; ++w) n += n_part[w];
     float term = 0.0f;
     if (g == 0 && e < p.E) {
         for (int i = 1; i < groups; ++i) {
@@ -186,113 +234,179 @@ __global__ __launch_bounds__(1024) void balance_segment_kernel(BalanceParams p) 
     }
     term = block_sum(term, fs);
     if (tid == 0) {
-        p.tokens[s] = n;
         term = n ? term * ((float)p.E / ((float)p.k * (float)n)) : 0.0f;
         if (p.S == 1) {
+            p.tokens[s] = n;
             *p.loss = p.coef * term;
         } else {
-            p.terms[s] = term;
-            __threadfence();
-            last = atomicAdd(p.arrived, 1) == p.S - 1;
+            // What the last block reads is written through to memory, and has been before this
+            // block counts itself: the wait stands in for a release of the whole L2.
+            __hip_atomic_store(&p.tokens[s], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(&p.terms[s], term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            last = __hip_atomic_fetch_add(p.arrived, 1, __ATOMIC_RELAXED,
+                                          __HIP_MEMORY_SCOPE_AGENT) == p.S - 1;
         }
     }
     if (p.S == 1) return;
     __syncthreads();
     if (!last) return;
-    __threadfence();
     float total = 0.0f;
     int used = 0;
-    for (int i = tid; i < p.S; i += 1024) {
+    for (int i = tid; i < p.S; i += threads) {
         total += __hip_atomic_load(&p.terms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         used += __hip_atomic_load(&p.tokens[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > 0;
     }
     total = block_sum(total, fs);
-    used = block_sum(used, is2);
+    used = block_sum(used, is);
     if (tid == 0) *p.loss = used ? p.coef * (total / (float)used) : 0.0f;
 }
 
-// Gradient of the logits, one token per 16-lane row.
-template <int PER_LANE>
+// Gradient of the logits, four consecutive tokens per wave.  All rows, choices and offsets are asked
+// for before the first is used.  Bound by its arithmetic (about 250 instructions per wave): 65536 x
+// 64, 38 MB, 12.2 us with both terms (a copy of 17 MB alone takes 4.6 us); waves of 2, 4 and 8 groups
+// with the next group's loads in flight took 14.6, 15.6 and 20 us.
+template <int PER_LANE, bool GATE, bool BALANCE>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradParams p) {
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int j16 = lane & 15, row = lane >> 4;
     int used = 1;
-    if (p.counts && p.S > 1) {                     // segments with tokens
+    if (BALANCE && p.S > 1) {                     // segments with tokens
         used = 0;
         for (int i = 0; i < p.S; i += kWave)
             used += __popcll(__ballot(i + lane < p.S && p.tokens[i + lane] > 0));
         used = max(used, 1);
     }
-    const float scale = p.counts ? p.coef * (p.grad_loss ? *p.grad_loss : 1.0f) / (float)used : 0.0f;
-    const int t = (blockIdx.x * 4 + wave) * 4 + row;
-    const bool live = t < p.T && (!p.active || p.active[t]);
-    float pr[PER_LANE], g[PER_LANE];
-    softmax_row<PER_LANE>(live ? p.logits + (size_t)t * p.E : nullptr, p.E, j16, pr);
-#pragma unroll
-    for (int i = 0; i < PER_LANE; ++i) g[i] = 0.0f;
-    if (p.counts) {
+    const float scale = BALANCE ? p.coef * (p.grad_loss ? *p.grad_loss : 1.0f) / (float)used : 0.0f;
+    // up to 63 segments: their offsets stay in the lanes
+    const bool few = p.S < kWave;
+    const int my_offset = (BALANCE && p.offsets && few) ? p.offsets[min(lane, p.S)] : 0;
+
+    struct Group {
+        float x[PER_LANE], w, gw;
+        int count[PER_LANE], id, n;
+        bool live;
+    };
+    auto fetch = [&](int t0, Group& g) {
+        const int t = t0 + row, tc = min(t, p.T - 1);
+        load_row<PER_LANE>(p.logits + (size_t)tc * p.E, p.E, j16, p.vec, g.x);
+        if constexpr (GATE) {
+            const size_t slot = (size_t)tc * p.k + min(j16, p.k - 1);
+            g.id = p.ids[slot];
+            g.w = p.topk_w[slot];
+            g.gw = p.grad_w[slot];
+        }
+        g.live = t < p.T && (!p.active || p.active[tc]);
+        if constexpr (!BALANCE) return;
         int s = 0;
         if (p.offsets) {
-            // last segment that starts at or before t: a 16-way search by the token's row
-            int none = 0;
-            for (int n = p.S + 1; n > 1;) {
-                const int step = (n + 15) / 16;
-                const int at = s + j16 * step;
-                const bool hit = j16 * step < n && at <= p.S && p.offsets[at] <= t;
-                const int hits = __popc((unsigned)(__ballot(hit) >> (row * 16)) & 0xffffu);
-                none |= hits == 0;
-                s += max(hits - 1, 0) * step;
-                n = step;
-            }
-            if (none || s >= p.S) s = -1;
-        }
-        const int n = (live && s >= 0) ? p.tokens[s] : 0;
-        float f[PER_LANE], dot = 0.0f;
-        const float fe = n > 0 ? (float)p.E / ((float)p.k * (float)n) : 0.0f;
+            // last segment that starts at or before the token (-1: none), for the wave's four
+            // tokens: a 64-way search each
+            int at[4] = {0, 0, 0, 0};
+            bool none[4] = {false, false, false, false};
+            if (few) {
 #pragma unroll
-        for (int i = 0; i < PER_LANE; ++i) {
-            const int e = j16 + 16 * i;
-            f[i] = (n > 0 && e < p.E) ? (float)p.counts[(size_t)s * p.E + e] * fe : 0.0f;
-            dot += f[i] * pr[i];
-        }
-        dot = row_total(dot);
-        const float c = n > 0 ? scale / (float)n : 0.0f;
-#pragma unroll
-        for (int i = 0; i < PER_LANE; ++i) g[i] = n > 0 ? c * pr[i] * (f[i] - dot) : 0.0f;
-    }
-    if (p.grad_w) {
-        int id = -1;
-        float w = 0.0f, gw = 0.0f;
-        if (live && j16 < p.k) {
-            id = p.ids[(size_t)t * p.k + j16];
-            if ((unsigned)id < (unsigned)p.E) {
-                w = p.topk_w[(size_t)t * p.k + j16];
-                gw = p.grad_w[(size_t)t * p.k + j16];
+                for (int r = 0; r < 4; ++r) {
+                    const int hits = __popcll(__ballot(lane <= p.S && my_offset <= t0 + r));
+                    none[r] = hits == 0;
+                    at[r] = hits - 1;
+                }
             } else {
+                for (int n = p.S + 1; n > 1;) {
+                    const int step = (n + kWave - 1) / kWave;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int o = at[r] + lane * step;
+                        const bool in = lane * step < n && o <= p.S;
+                        const int hits = __popcll(__ballot(in && p.offsets[min(o, p.S)] <= t0 + r));
+                        none[r] |= hits == 0;
+                        at[r] += max(hits - 1, 0) * step;
+                    }
+                    n = step;
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (row == r) s = none[r] || at[r] >= p.S ? -1 : at[r];
+        }
+        const int sc = max(s, 0);
+        g.n = p.tokens[sc];
+        if (s < 0) g.n = 0;
+        load_row<PER_LANE>(p.counts + (size_t)sc * p.E, p.E, j16, p.vec, g.count);
+    };
+    auto compute = [&](int t0, Group& in) {
+        const int t = t0 + row;
+        float pr[PER_LANE], g[PER_LANE];
+        softmax_row<PER_LANE>(in.x, in.live, p.E, j16, pr);
+#pragma unroll
+        for (int i = 0; i < PER_LANE; ++i) g[i] = 0.0f;
+        if constexpr (BALANCE) {
+            const int n = in.live ? in.n : 0;
+            const float fe = n > 0 ? (float)p.E / ((float)p.k * (float)n) : 0.0f;
+            float f[PER_LANE], dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < PER_LANE; ++i) {
+                f[i] = (n > 0 && j16 * PER_LANE + i < p.E) ? (float)in.count[i] * fe : 0.0f;
+                dot += f[i] * pr[i];
+            }
+            dot = row_total(dot);
+            const float c = n > 0 ? scale / (float)n : 0.0f;
+#pragma unroll
+            for (int i = 0; i < PER_LANE; ++i) g[i] = n > 0 ? c * pr[i] * (f[i] - dot) : 0.0f;
+        }
+        if constexpr (GATE) {
+            int id = in.id;
+            float w = in.w, gw = in.gw;
+            if (!in.live || j16 >= p.k || (unsigned)id >= (unsigned)p.E) {
                 id = -1;
+                w = gw = 0.0f;
+            }
+            const float u = row_total(w * gw);
+            const float mine = p.gate_all ? w * gw : w * (gw - u);
+            auto choice = [&](auto jc) {               // slot j of the row's token
+                constexpr int J = decltype(jc)::value;
+                if (J >= p.k) return;
+                const int idj = row_lane<J>(id);
+                const float v = __builtin_bit_cast(float, row_lane<J>(__builtin_bit_cast(int, mine)));
+#pragma unroll
+                for (int i = 0; i < PER_LANE; ++i)
+                    if (j16 * PER_LANE + i == idj) g[i] += v;
+            };
+            static_assert(MOE_MAX_TOPK == 8, "slots below");
+            choice(std::integral_constant<int, 0>{});
+            choice(std::integral_constant<int, 1>{});
+            choice(std::integral_constant<int, 2>{});
+            choice(std::integral_constant<int, 3>{});
+            choice(std::integral_constant<int, 4>{});
+            choice(std::integral_constant<int, 5>{});
+            choice(std::integral_constant<int, 6>{});
+            choice(std::integral_constant<int, 7>{});
+            if (p.gate_all) {
+#pragma unroll
+                for (int i = 0; i < PER_LANE; ++i) g[i] -= pr[i] * u;
             }
         }
-        const float u = row_total(w * gw);
-        const float mine = p.gate_all ? w * gw : w * (gw - u);
-        for (int j = 0; j < p.k; ++j) {
-            const int idj = __shfl(id, row * 16 + j);
-            const float v = __shfl(mine, row * 16 + j);
+        if (t >= p.T) return;
+        float* dst = p.grad + (size_t)t * p.E + j16 * PER_LANE;
+        if constexpr (PER_LANE >= 4) {
+            if (p.vec) {
 #pragma unroll
-            for (int i = 0; i < PER_LANE; ++i)
-                if (j16 + 16 * i == idj) g[i] += v;
+                for (int i = 0; i < PER_LANE; i += 4)
+                    if (j16 * PER_LANE + i < p.E)
+                        *(f32x4*)(dst + i) = f32x4{g[i], g[i + 1], g[i + 2], g[i + 3]};
+                return;
+            }
         }
-        if (p.gate_all) {
 #pragma unroll
-            for (int i = 0; i < PER_LANE; ++i) g[i] -= pr[i] * u;
-        }
-    }
-    if (t < p.T) {
-#pragma unroll
-        for (int i = 0; i < PER_LANE; ++i) {
-            const int e = j16 + 16 * i;
-            if (e < p.E) p.grad[(size_t)t * p.E + e] = g[i];
-        }
-    }
+        for (int i = 0; i < PER_LANE; ++i)
+            if (j16 * PER_LANE + i < p.E) dst[i] = g[i];
+    };
+
+    const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * 4;
+    if (first >= p.T) return;
+    Group g;
+    fetch((int)first, g);
+    compute((int)first, g);
 }
 
 // Gradients of the combine, one token per block: each thread takes 8 columns at a time, reads the
@@ -364,11 +478,16 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineGradParams
 
 // ------------------------------------------------------------------------------------ host
 
-// Tokens per cell: about 512 pieces at most (beside one per segment), at least 16 tokens each.
-int balance_cell(int T) { return T <= 8192 ? 16 : (int)(((int64_t)T + 8191) / 8192) * 16; }
+// Tokens per cell: about 1024 pieces at most (beside one per segment), 512 where few segments' blocks
+// add them up (65536 x 64: one segment 13.3 against 15.1 us, 48 segments 15.4 against 14.5); at least
+// 16 tokens each.
+static int balance_cell(int T, int S) {
+    const int64_t turns = S < 8 ? 8192 : 16384;
+    return (int)(((int64_t)T + turns - 1) / turns) * 16 + (T == 0 ? 16 : 0);
+}
 
 size_t balance_workspace_layout(int T, int E, int S, BalanceParams* p, char* base) {
-    const int cell = balance_cell(T);
+    const int cell = balance_cell(T, S);
     const int64_t pieces = (int64_t)((int64_t)T + cell - 1) / cell + S;
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     size_t at = 0;
@@ -394,21 +513,35 @@ size_t balance_workspace_layout(int T, int E, int S, BalanceParams* p, char* bas
     return at;
 }
 
-hipError_t launch_balance(const BalanceParams& p, hipStream_t s) {
+static bool in_pieces(int E, const void* a, const void* b) {
+    return E % 4 == 0 && (((uintptr_t)a | (uintptr_t)b) & 15) == 0;
+}
+
+hipError_t launch_balance(const BalanceParams& args, hipStream_t s) {
+    BalanceParams p = args;
+    p.vec = in_pieces(p.E, p.logits, nullptr);
     if (p.E <= 16) balance_piece_kernel<1><<<p.pieces, 256, 0, s>>>(p);
     else if (p.E <= 64) balance_piece_kernel<4><<<p.pieces, 256, 0, s>>>(p);
     else if (p.E <= 128) balance_piece_kernel<8><<<p.pieces, 256, 0, s>>>(p);
     else balance_piece_kernel<16><<<p.pieces, 256, 0, s>>>(p);
-    balance_segment_kernel<<<p.S, 1024, 0, s>>>(p);
+    balance_segment_kernel<<<p.S, p.pieces / p.S > 64 ? 1024 : 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
-hipError_t launch_route_backward(const RouteGradParams& p, hipStream_t s) {
+hipError_t launch_route_backward(const RouteGradParams& args, hipStream_t s) {
+    RouteGradParams p = args;
+    p.vec = in_pieces(p.E, p.logits, p.grad) && ((uintptr_t)p.counts & 15) == 0;
     const int grid = (int)(((int64_t)p.T + 15) / 16);
-    if (p.E <= 16) route_backward_kernel<1><<<grid, 256, 0, s>>>(p);
-    else if (p.E <= 64) route_backward_kernel<4><<<grid, 256, 0, s>>>(p);
-    else if (p.E <= 128) route_backward_kernel<8><<<grid, 256, 0, s>>>(p);
-    else route_backward_kernel<16><<<grid, 256, 0, s>>>(p);
+    auto go = [&](auto gate, auto balance) {
+        constexpr bool G = decltype(gate)::value, B = decltype(balance)::value;
+        if (p.E <= 16) route_backward_kernel<1, G, B><<<grid, 256, 0, s>>>(p);
+        else if (p.E <= 64) route_backward_kernel<4, G, B><<<grid, 256, 0, s>>>(p);
+        else if (p.E <= 128) route_backward_kernel<8, G, B><<<grid, 256, 0, s>>>(p);
+        else route_backward_kernel<16, G, B><<<grid, 256, 0, s>>>(p);
+    };
+    if (p.grad_w && p.counts) go(std::true_type{}, std::true_type{});
+    else if (p.grad_w) go(std::true_type{}, std::false_type{});
+    else go(std::false_type{}, std::true_type{});
     return hipGetLastError();
 }
 

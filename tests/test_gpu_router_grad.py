@@ -152,6 +152,9 @@ def test_balance_all_padding_masked_rows_and_empty_batch():
     assert torch.equal(counts.cpu(), wc) and int(tokens) == 20
     assert abs(float(loss) - wl) <= 64 * U * wl and not g[3:5].any() and float(g[5, 2]) == 0
     assert ((probs.cpu().double() - wp).abs() <= 40 * U * wp).all()
+    logits[0, 1] = float("inf")                        # no softmax: NaN, not a plausible number
+    loss, _, probs, _ = q.moe_balance_loss(logits, ids, 0.5)
+    assert torch.isnan(loss).all() and torch.isnan(probs[0, 1])
     for S, off in ((1, None), (3, torch.zeros(4, dtype=torch.int32, device="cuda"))):
         e = torch.empty((0, 12), device="cuda")
         ei = torch.empty((0, 2), dtype=torch.int32, device="cuda")
