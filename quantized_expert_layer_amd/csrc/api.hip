@@ -834,7 +834,8 @@ int32_t moe_linear_backward(const void* grad_out, int64_t ldg, int32_t grad_dtyp
         if (moe::launch_linear_dz(z, dtype, grad_bias, s) != hipSuccess) return MOE_ERR_HIP;
     }
     const uint16_t* dz = f.need_dz ? f.dz.dz : (const uint16_t*)grad_out;
-    if (grad_a && M > 0) {
+    const bool want_a = grad_a && M > 0, want_w = grad_w && N > 0;
+    if (want_a) {
         f.da.a = dz;
         f.da.b = w;
         if (f.pack_w) {
@@ -842,9 +843,8 @@ int32_t moe_linear_backward(const void* grad_out, int64_t ldg, int32_t grad_dtyp
             f.da.b = f.pack_w;
         }
         grad_out_epilogue(f.da.epi, grad_a, K);
-        if (moe::launch_linear_product(f.da, dtype, s) != hipSuccess) return MOE_ERR_HIP;
     }
-    if (grad_w && N > 0) {
+    if (want_w) {
         f.dw.a = dz;
         f.dw.b = a;
         if (f.pack_a) {
@@ -852,8 +852,11 @@ int32_t moe_linear_backward(const void* grad_out, int64_t ldg, int32_t grad_dtyp
             f.dw.b = f.pack_a;
         }
         grad_out_epilogue(f.dw.epi, grad_w, K);
-        if (moe::launch_linear_product(f.dw, dtype, s) != hipSuccess) return MOE_ERR_HIP;
     }
+    if (want_a && want_w && moe::linear_pair(f.da, f.dw))
+        return hip_status(moe::launch_linear_pair(f.da, f.dw, dtype, s));
+    if (want_a && moe::launch_linear_product(f.da, dtype, s) != hipSuccess) return MOE_ERR_HIP;
+    if (want_w && moe::launch_linear_product(f.dw, dtype, s) != hipSuccess) return MOE_ERR_HIP;
     return MOE_OK;
 }
 

@@ -156,6 +156,7 @@ struct LinearProduct {       // C[i, j] = sum over parts and r < red of A[i, r] 
     float* part;             // fp32 [split, M, ldpart] when split > 1
     int ldpart, split, cfg, tiles_m, tiles_n;
     int whole;               // tiles computed whole; the rest in quarters (256 x 256 tiles)
+    double us;               // what the plan expects
 };
 
 struct LinearDz {
@@ -176,6 +177,10 @@ struct LinearDz {
 void linear_plan(LinearProduct& p);
 size_t linear_part_bytes(const LinearProduct& p);
 hipError_t launch_linear_product(const LinearProduct& p, int dtype, hipStream_t stream);
+// Both gradients in one launch, if that is the better plan for them (which it then becomes).
+bool linear_pair(LinearProduct& da, LinearProduct& dw);
+hipError_t launch_linear_pair(const LinearProduct& da, const LinearProduct& dw, int dtype,
+                              hipStream_t stream);
 hipError_t launch_linear_pack(const uint16_t* src, int64_t ld, int rows, int cols, uint16_t* dst,
                               hipStream_t stream);
 int linear_dz_blocks(int M, int N);

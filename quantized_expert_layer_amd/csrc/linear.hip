@@ -213,6 +213,23 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearProduct
     tile_body<DT, ACOLS, BCOLS, BM, BN, WM, WN, NBUF>(p, lds, z, tm * BM, tn * BN);
 }
 
+// Both gradients' products in one launch, 128 x 128 tiles, two blocks per CU: each alone leaves the
+// chip half empty where neither fills it (3777 x 1024 x 4096 fp16: 39 + 41 us one after the other).
+template <int DT>
+__global__ __launch_bounds__(512) void linear_pair_kernel(LinearProduct da, LinearProduct dw) {
+    __shared__ __attribute__((aligned(1024))) char lds[(128 + 128) * kBK * 2 * 2];
+    const int na = (da.whole + 7) / 8 * 8;                     // keeps dw's blocks on their XCDs
+    int tm, tn;
+    if ((int)blockIdx.x < na) {
+        if ((int)blockIdx.x >= da.whole) return;
+        tile_of(da, blockIdx.x, da.whole, tm, tn);
+        tile_body<DT, false, true, 128, 128, 2, 4, 2>(da, lds, 0, tm * 128, tn * 128);
+    } else {
+        tile_of(dw, blockIdx.x - na, dw.whole, tm, tn);
+        tile_body<DT, true, true, 128, 128, 2, 4, 2>(dw, lds, 0, tm * 128, tn * 128);
+    }
+}
+
 // Sums the splits' partial products in their order and applies the epilogue.
 template <int DT>
 __global__ __launch_bounds__(256) void linear_reduce_kernel(LinearProduct p) {
@@ -550,6 +567,7 @@ void linear_plan(LinearProduct& p) {
             us += (double)((whole + kCus - 1) / kCus) * (t.base + t.stage * st);
             if (us < best) {
                 best = us;
+                p.us = us;
                 p.cfg = c;
                 p.split = split;
                 p.tiles_m = tm;
@@ -576,6 +594,37 @@ hipError_t launch_linear_product(const LinearProduct& p, int dtype, hipStream_t 
     };
     if (dtype == MOE_DT_BF16) go(std::integral_constant<int, MOE_DT_BF16>{});
     else go(std::integral_constant<int, MOE_DT_FP16>{});
+    return hipGetLastError();
+}
+
+// Whether the gradients' two products (neither split) run as one launch: all tiles at once on the
+// chip, and sooner than one after the other.
+bool linear_pair(LinearProduct& da, LinearProduct& dw) {
+    const TileCost& t = kTiles[2];
+    auto tiles = [&](const LinearProduct& p) {
+        return (int64_t)((p.M + t.bm - 1) / t.bm) * ((p.N + t.bn - 1) / t.bn);
+    };
+    auto stages = [](const LinearProduct& p) { return (p.red + kBK - 1) / kBK * p.parts; };
+    const int64_t n = tiles(da) + tiles(dw);
+    if (n > 2 * kCus - 8) return false;
+    const int st = stages(da) > stages(dw) ? stages(da) : stages(dw);
+    const double us = n > kCus ? t.base2 + t.stage2 * st : t.base + t.stage * st;
+    if (us > da.us + dw.us) return false;
+    for (LinearProduct* p : {&da, &dw}) {
+        p->tiles_m = (p->M + t.bm - 1) / t.bm;
+        p->tiles_n = (p->N + t.bn - 1) / t.bn;
+        p->whole = p->tiles_m * p->tiles_n;
+        p->split = 1;
+        p->part = nullptr;
+    }
+    return true;
+}
+
+hipError_t launch_linear_pair(const LinearProduct& da, const LinearProduct& dw, int dtype,
+                              hipStream_t s) {
+    const int grid = (da.whole + 7) / 8 * 8 + dw.whole;
+    if (dtype == MOE_DT_BF16) linear_pair_kernel<MOE_DT_BF16><<<grid, 512, 0, s>>>(da, dw);
+    else linear_pair_kernel<MOE_DT_FP16><<<grid, 512, 0, s>>>(da, dw);
     return hipGetLastError();
 }
 
