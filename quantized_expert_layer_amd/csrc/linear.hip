@@ -230,6 +230,98 @@ __global__ __launch_bounds__(512) void linear_pair_kernel(LinearProduct da, Line
     }
 }
 
+// ------------------------------------------------------------------------------------
+// Input gradient of a narrow layer (N <= 64, a router): da = dz w is a write of M x K with next to no
+// arithmetic.  A block holds its 256 columns of w in registers (through one LDS stage and the
+// transposing reads) and walks down `rows` rows, 16 at a time, the next rows' dz on its way.  The
+// four products of a 16 x 64 piece take columns 16 g + 4 j + i (g the lane's quarter, j the product,
+// i its result), so a lane ends up with 16 consecutive columns and a row leaves as whole lines.
+// Bound by the write: 8192 x 4096 from fp32 gradients of 16 experts, 67 MB, 22 us (30 us in tiles).
+// ------------------------------------------------------------------------------------
+template <int DT>
+__global__ __launch_bounds__(256) void linear_thin_kernel(LinearProduct p, int rows) {
+#ifdef __HIP_DEVICE_COMPILE__
+    using OB = Operand<256, true, 4>;
+    __shared__ __attribute__((aligned(1024))) char lds[OB::kBytes];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int n0 = blockIdx.x * 256;
+    OB ob;
+    ob.init(p.b, p.ldb, n0, p.b_outs, p.b_red, wave, lane);
+    const auto wb = ob.stage(ob.base, p.b_red, p.b_red > 0);
+#pragma unroll
+    for (int i = 0; i < OB::kLoads; ++i)
+        ob.load(wb, i, p.b_red, (uint32_t)(uintptr_t)(lds_void*)lds, wave);
+    // dz: row lane & 15, summed indices 8 (lane >> 4) .. + 7 of each half; past the end zeros
+    const int64_t m0 = (int64_t)blockIdx.y * rows;
+    const int left = (int)min((int64_t)rows, p.M - m0);
+    const int ld = (int)p.lda, kl = 8 * (lane >> 4);
+    const uint32_t bytes = ((uint32_t)(left - 1) * ld + p.red) * 2u;
+    const auto z0 = buffer_of(p.a + m0 * ld, bytes), z1 = buffer_of(p.a + p.a_part + m0 * ld, bytes);
+    auto fetch = [&](int r, s16x8 (&z)[2][2]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t at = r + (lane & 15) < left && 32 * h + kl < p.red
+                ? (uint32_t)((r + (lane & 15)) * ld + 32 * h + kl) * 2u : kOutside;
+            z[0][h] = __builtin_bit_cast(s16x8, __builtin_amdgcn_raw_buffer_load_b128(z0, at, 0, 0));
+            z[1][h] = __builtin_bit_cast(s16x8, __builtin_amdgcn_raw_buffer_load_b128(
+                z1, p.parts == 2 ? at : kOutside, 0, 0));
+        }
+    };
+    s16x8 z[2][2], nz[2][2];
+    fetch(0, z);
+    __builtin_amdgcn_s_waitcnt(0x0070);
+    __syncthreads();
+    s16x8 w[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 32 * h + 8 * (lane >> 4) + ((lane >> 2) & 3);
+            const uint32_t s = (((lane >> 2) & 3) | ((lane >> 4) << 2)) & OB::kPairMask;
+            const char* q = lds + r * 512 + (((uint32_t)(wave * 4 + (lane & 3)) ^ s) << 5) + j * 8;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)q);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(q + 4 * 512));
+            w[h][j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    const int col = n0 + wave * 64 + (lane >> 4) * 16;
+    for (int r = 0; r < left; r += 16) {
+        fetch(r + 16, nz);                                     // past the end: nothing is read
+        f32x4 acc[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) acc[j] = mfma_dt<DT>(w[h][j], z[0][h], acc[j]);
+            if (p.parts == 2) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) acc[j] = mfma_dt<DT>(w[h][j], z[1][h], acc[j]);
+            }
+        }
+        const int row = r + (lane & 15);
+        if (row < left) {
+            uint16_t* dst = (uint16_t*)p.epi.out + (m0 + row) * p.epi.ldo + col;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float v[8] = {acc[2 * c][0], acc[2 * c][1], acc[2 * c][2], acc[2 * c][3],
+                                    acc[2 * c + 1][0], acc[2 * c + 1][1], acc[2 * c + 1][2], acc[2 * c + 1][3]};
+                if (p.epi.vec && col + 8 * c + 8 <= p.N) {
+                    *(u32x4*)(dst + 8 * c) = pack16<DT>(v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (col + 8 * c + i < p.N) dst[8 * c + i] = f32_to_dt<DT>(v[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) z[i][h] = nz[i][h];
+    }
+#endif
+}
+
 // Sums the splits' partial products in their order and applies the epilogue.
 template <int DT>
 __global__ __launch_bounds__(256) void linear_reduce_kernel(LinearProduct p) {
@@ -501,7 +593,7 @@ constexpr int kCus = 256;
 // linear_stream_kernel instead of a tile, for products of up to 32 rows and kStreamMost terms.  On
 // the device (bf16, us, stream against tile): 1 x 4096 x 4096 8.8 / 12.0, 17 x 2048 x 2048 8.7 / 8.7,
 // 16 x 4096 x 4096 11.4 / 12.5, 16 x 4096 x 6400 20.0 / 15.6 -- and one launch less on the host.
-constexpr int kStream = 100;
+constexpr int kStream = 100, kThin = 101;            // kThin: linear_thin_kernel
 constexpr int64_t kStreamMost = (int64_t)1 << 28;
 
 // Waves per block: about 4096 in all, 4 to 16 a block, at most one per stage of K.
@@ -513,6 +605,15 @@ void launch_stream(const LinearProduct& p, hipStream_t s) {
     if (waves > stages) waves = stages;
     if (p.M <= 16) linear_stream_kernel<DT, 1><<<grid, waves * kWave, 0, s>>>(p);
     else linear_stream_kernel<DT, 2><<<grid, waves * kWave, 0, s>>>(p);
+}
+
+// About 1024 blocks of at least 64 rows, and at most 2^15 (a block's byte offsets stay below 2^31).
+template <int DT>
+void launch_thin(const LinearProduct& p, hipStream_t s) {
+    const int wide = (p.N + 255) / 256;
+    int64_t rows = ((int64_t)p.M * wide / 1024 + 63) / 64 * 64;
+    rows = rows < 64 ? 64 : rows > 1 << 15 ? 1 << 15 : rows;
+    linear_thin_kernel<DT><<<dim3(wide, (unsigned)((p.M + rows - 1) / rows)), 256, 0, s>>>(p, (int)rows);
 }
 
 template <int DT, bool AC, bool BC>
@@ -534,6 +635,12 @@ void linear_plan(LinearProduct& p) {
     if (!p.a_cols && !p.b_cols && p.M <= 32 && (int64_t)p.M * p.N * p.red <= kStreamMost) {
         p.cfg = kStream;
         p.split = 1;
+        return;
+    }
+    if (!p.a_cols && p.b_cols && p.red <= kBK && p.lda <= 1 << 14 && (int64_t)p.M * p.N >= 1 << 22) {
+        p.cfg = kThin;                       // a write of M x N; a tile's loads and epilogue would not
+        p.split = 1;                         // overlap (8192 x 4096 from 16: 30 us in 256 x 256 tiles)
+        p.us = 4.0 + 2.0 * p.M * p.N / 4.4e6;
         return;
     }
     const int stages = ((p.red + kBK - 1) / kBK) * p.parts;
@@ -586,6 +693,7 @@ hipError_t launch_linear_product(const LinearProduct& p, int dtype, hipStream_t 
     auto go = [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         if (p.cfg == kStream) launch_stream<DT>(p, s);
+        else if (p.cfg == kThin) launch_thin<DT>(p, s);
         else if (!p.a_cols && !p.b_cols) launch_tiles<DT, false, false>(p, s);
         else if (!p.a_cols) launch_tiles<DT, false, true>(p, s);
         else launch_tiles<DT, true, true>(p, s);

@@ -114,7 +114,7 @@ def _check_forward(M, K, N, dtype, out="same", act="none", bias=True, residual=T
 
 SIZES = [(1, 64, 16), (1, 4096, 16), (17, 2048, 2048), (3, 8, 1), (5, 7, 9), (64, 72, 65),
          (130, 1000, 257), (257, 129, 131), (300, 64, 300), (16, 6400, 48), (33, 640, 4096),
-         (1900, 200, 1808), (4000, 72, 3402)]
+         (1900, 200, 1808), (4000, 72, 3402), (70, 6400, 520), (31, 1024, 2050), (4352, 72, 4120)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -264,7 +264,8 @@ def _check_backward(M, K, N, dtype, grad="same", act="none", pads=(0, 0, 0, 0), 
 
 
 BACK_SIZES = [(1, 64, 16), (17, 2048, 64), (5, 7, 9), (544, 256, 60), (3, 8, 1), (130, 1000, 257),
-              (257, 129, 131), (1000, 1808, 72), (3000, 136, 24), (1900, 1808, 72), (700, 520, 648)]
+              (257, 129, 131), (1000, 1808, 72), (3000, 136, 24), (1900, 1808, 72), (700, 520, 648),
+              (4100, 2056, 136), (4100, 1032, 16), (2100, 2053, 60), (70000, 72, 64), (300, 72, 6400)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -278,7 +279,7 @@ def test_linear_backward_sizes(M, K, N, dtype):
 @pytest.mark.parametrize("grad", ["same", "fp32"])
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
 def test_linear_backward_activations_and_fp32_gradients(act, grad, dtype):
-    for M, K, N in ((40, 136, 60), (300, 72, 264)):
+    for M, K, N in ((40, 136, 60), (300, 72, 264), (4111, 1048, 24)):
         case(f"linear backward {act} grad {grad} {dtype} {M}x{K}x{N}")
         _check_backward(M, K, N, dtype, grad=grad, act=act)
 
@@ -391,3 +392,57 @@ def test_linear_in_a_captured_graph():
         want = step()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(outs, want)), i
+
+
+def test_linear_offsets_past_32_bits():
+    """A batch of 2.4e9 elements: rows at both ends against the reference, and a weight gradient that
+    only the last rows feed (every other row's gradient is zero)."""
+    import torch
+    M, K, N = 590001, 4096, 24
+    case(f"linear {M}x{K}x{N}")
+    g = torch.Generator(device="cuda").manual_seed(11)
+    a = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, 1, M // 2, M - 130, M - 2, M - 1], device="cuda")
+    a[rows] = _rand(g, (len(rows), K), 1.0, torch.bfloat16)
+    w = _rand(g, (N, K), K ** -0.5, torch.bfloat16)
+    out = q.moe_linear(a, w, out_dtype=torch.float32)
+    ref = a[rows].double() @ w.double().t().contiguous()
+    tol = _sum_bound(K) * (a[rows].double().abs() @ w.double().abs().t().contiguous())
+    _close(out[rows], ref, tol + 2.0 ** -23 * ref.abs(), "last rows")
+    live = torch.ones(M, dtype=torch.bool, device="cuda")
+    live[rows] = False
+    assert not out[live].any()
+    go = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    go[rows] = _rand(g, (len(rows), N), 1.0, torch.bfloat16)
+    ga, gw, gb = q.moe_linear_backward(go, a, w)
+    r64 = go[rows].double()
+    ref = r64.t().contiguous() @ a[rows].double()
+    mag = r64.abs().t().contiguous() @ a[rows].double().abs()
+    _close(gw, ref, _sum_bound(M) * mag + _half_step(ref.abs(), torch.bfloat16) * 1.01, "weight gradient")
+    ref = r64 @ w.double().contiguous()
+    mag = r64.abs() @ w.double().abs()
+    _close(ga[rows], ref, _sum_bound(N) * mag + _half_step(ref.abs(), torch.bfloat16) * 1.01, "input gradient")
+    assert not ga[live].any()
+
+
+def test_linear_two_streams_at_once():
+    """Calls that overlap on two streams, each with the workspace the binding gives it."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(12)
+    a = [_rand(g, (300, 1001), 1.0, torch.float16) for _ in range(2)]
+    w = [_rand(g, (200, 1001), 0.03, torch.float16) for _ in range(2)]
+    go = [_rand(g, (300, 200), 0.1, torch.float16) for _ in range(2)]
+    call = lambda i, s=None: (q.moe_linear(a[i], w[i], act="gelu", stream=s),) \
+        + q.moe_linear_backward(go[i], a[i], w[i], stream=s)
+    case("linear on two streams")
+    want = [call(0), call(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i in range(2):
+            got[i].append(call(i, streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for outs in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(outs, want[i]))

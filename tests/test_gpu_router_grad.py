@@ -381,3 +381,75 @@ def test_router_tuning_step(name, T):
     with pytest.raises(ValueError):                  # a layer that only makes the decode call
         only = q.DeviceLayer.from_inputs(inp, decode=True)
         only.router_backward(out, lg, ws)
+
+
+def test_router_offsets_past_32_bits():
+    """Logits of 4.6 GB: counts in all, and the gradient of tokens at both ends."""
+    import torch
+    T, E, k = 4_500_001, 256, 2
+    case(f"balance T={T} E={E}")
+    logits = torch.zeros((T, E), device="cuda")
+    ends = torch.tensor([0, 1, T // 2, T - 3, T - 1], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    logits[ends] = torch.randn((len(ends), E), generator=g, device="cuda")
+    ids = (torch.arange(T * k, device="cuda") % E).to(torch.int32).reshape(T, k)
+    loss, counts, probs, tokens = q.moe_balance_loss(logits, ids, 1.0)
+    assert torch.equal(counts[0].long(), torch.bincount(ids.flatten().long(), minlength=E))
+    assert int(tokens) == T
+    # nearly uniform probabilities and counts: the loss is 1 up to the five rows' part and rounding
+    assert abs(float(loss) - 1) <= 1e-5
+    w = torch.rand((T, k), generator=g, device="cuda")
+    gw = torch.randn((T, k), generator=g, device="cuda")
+    grad = q.moe_route_backward(logits, ids, topk_w=w, grad_w=gw, counts=counts, tokens=tokens, coef=1.0)
+    ref, mag = _ref_gate(logits[ends], ids[ends].cpu(), w[ends].cpu(), gw[ends].cpu(), "topk")
+    f = counts[0].cpu().double() * E / (k * T)
+    p = _softmax64(logits[ends]).cpu()
+    ref += p * (f - (p @ f)[:, None]) / T
+    assert ((grad[ends].cpu().double() - ref).abs() <= (E + 24) * U * (mag + 2 * p / T) + 1e-45).all()
+
+
+def test_combine_offsets_past_32_bits():
+    import torch
+    T, k, d = 66000, 8, 4096
+    case(f"combine gradients T={T} k={k} d={d}")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    y = torch.zeros((T * k, d), dtype=torch.float16, device="cuda")
+    inv = torch.arange(T * k - 1, -1, -1, dtype=torch.int32, device="cuda")
+    go = torch.zeros((T, d), dtype=torch.float16, device="cuda")
+    for t in (0, T - 1):
+        go[t] = torch.randn(d, generator=g, device="cuda").half()
+        for j in range(k):
+            y[int(inv[t * k + j])] = torch.randn(d, generator=g, device="cuda").half()
+    w = torch.rand((T, k), generator=g, device="cuda")
+    gw, gy = q.moe_combine_backward(go, y, inv, w)
+    for t in (0, T - 1):
+        rows = y[inv[t * k:(t + 1) * k].long()].double()
+        ref, mag = (rows * go[t].double()).sum(dim=1), (rows * go[t].double()).abs().sum(dim=1)
+        assert ((gw[t].double() - ref).abs() <= (d / 64 + 16) * U * mag).all()
+        want = (w[t][:, None] * go[t].float()[None, :]).half()
+        assert torch.equal(gy[inv[t * k:(t + 1) * k].long()], want)
+    assert not gw[1:T - 1].any()
+
+
+def test_router_calls_on_a_side_stream_give_the_same_bits():
+    import torch
+    logits, ids, active = _inputs(700, 60, 4, 5, masked=0.05)
+    ids, w = q.moe_route_topk(logits, 4, "all", active=active)
+    gw = torch.randn((700, 4), generator=torch.Generator(device="cuda").manual_seed(6), device="cuda")
+    off = torch.tensor([0, 3, 300, 300, 690], dtype=torch.int32, device="cuda")
+
+    def step(s=None):
+        loss, counts, probs, tokens = q.moe_balance_loss(logits, ids, 0.3, active=active,
+                                                         seq_offsets=off, stream=s)
+        g = q.moe_route_backward(logits, ids, gate_mode="all", topk_w=w, grad_w=gw, active=active,
+                                 counts=counts, tokens=tokens, coef=0.3, seq_offsets=off, stream=s)
+        return loss, counts, probs, tokens, g
+
+    case("router calls on a side stream")
+    want = step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for s in (side, side.cuda_stream):
+        got = step(s)
+        side.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
