@@ -477,8 +477,9 @@ size_t moe_linear_workspace_size(int32_t M, int32_t N, int32_t K, int64_t lda, i
  *   grad_bias  16-bit [N], or NULL
  *   ws         at least moe_linear_backward_workspace_size(...) bytes, as for moe_linear
  *   Sums are fp32.  grad_bias sums the unrounded dz.  The products read dz in dtype: a 16-bit
- *   gradient with MOE_ACT_NONE or RELU is exact there, one through SILU or GELU is rounded once
- *   more, an fp32 gradient enters as two 16-bit parts (its first 16 bits in bf16, 22 in fp16).
+ *   gradient with MOE_ACT_NONE or RELU is exact there; an fp32 gradient enters as two 16-bit parts
+ *   (its first 16 bits in bf16, 22 in fp16), and so does one through SILU or GELU with M < 256,
+ *   which is rounded once to dtype with more rows.
  *   fp16 has a short range: scale the loss so that dz lies within it, as fp16 training does.
  *   With M == 0 grad_w and grad_bias, and with N == 0 grad_a, are written as zeros.
  * Errors: as moe_linear, plus MOE_ERR_INVALID when no gradient is wanted, or for an activation

@@ -669,7 +669,11 @@ LinearBackward linear_backward(int32_t M, int32_t N, int32_t K, int64_t lda, int
     LinearBackward f{};
     const int N8 = up8(N), K8 = up8(K);
     f.need_dz = grad_dtype == MOE_DT_FP32 || act != MOE_ACT_NONE || !in_pieces(N, ldg);
-    const int parts = grad_dtype == MOE_DT_FP32 ? 2 : 1;
+    // Through SILU or GELU dz is a product with no 16-bit form.  Rounded once it costs the gradients
+    // as much as their own rounding does (1.4 times the error in all); below 256 rows, where the
+    // products wait for memory, it is kept in two parts like an fp32 gradient.
+    const bool curved = act == MOE_ACT_SILU || act == MOE_ACT_GELU;
+    const int parts = grad_dtype == MOE_DT_FP32 || (curved && M < 256) ? 2 : 1;
     f.dz.cols8 = N8;
     f.dz.parts = parts;
     const int64_t ldz = f.need_dz ? N8 : ldg;

@@ -445,9 +445,9 @@ __global__ __launch_bounds__(256) void linear_pack_kernel(const uint16_t* __rest
 // dz = grad * act'(preact) as the 16-bit operand of the gradients' products, and this block's
 // column sums of it (fp32, unrounded).  An fp32 gradient is held as two 16-bit parts, dz = hi + lo
 // (lo = the rounding error of hi, itself rounded): 16 (bf16) or 22 (fp16) bits of it reach the
-// products, which then run over both parts.  A 16-bit gradient through an activation is rounded
-// once more to its own type: the products take nothing wider, and the error averages out over
-// the sums (each term's is at most half a step, the same as the output's own rounding).
+// products, which then run over both parts.  A 16-bit gradient through a curved activation is held
+// the same way, or with many rows rounded once to its own type (the products take nothing wider):
+// each term's error is then at most half a step, and averages to about the output's own rounding.
 // A thread takes 8 columns of a row; the block's 256 threads stand 2^lc across the columns and the
 // rest down the rows.  Bound by memory: 3840 x 4096 fp16 through ReLU, 94 MB, was 34 us with one
 // value per thread at a time.
