@@ -718,6 +718,11 @@ LinearBackward linear_backward(int32_t M, int32_t N, int32_t K, int64_t lda, int
     return f;
 }
 
+// A matrix to copy into `dst` (NULL: none).
+moe::LinearPack packed(const uint16_t* src, int64_t ld, int32_t rows, int32_t cols, uint16_t* dst) {
+    return moe::LinearPack{src, ld, dst ? rows : 0, cols, up8(cols), dst};
+}
+
 void grad_out_epilogue(moe::LinearEpilogue& e, uint16_t* out, int32_t K) {
     e.out = out;
     e.ldo = K;
@@ -763,16 +768,11 @@ int32_t moe_linear(const uint16_t* a, int64_t lda, const uint16_t* w, int64_t ld
     if (int32_t st = check_device()) return st;
     hipStream_t s = (hipStream_t)stream;
     moe::LinearProduct& p = f.p;
-    p.a = a;
-    p.b = w;
-    if (f.pack_a) {
-        if (moe::launch_linear_pack(a, lda, M, K, f.pack_a, s) != hipSuccess) return MOE_ERR_HIP;
-        p.a = f.pack_a;
-    }
-    if (f.pack_w) {
-        if (moe::launch_linear_pack(w, ldw, N, K, f.pack_w, s) != hipSuccess) return MOE_ERR_HIP;
-        p.b = f.pack_w;
-    }
+    p.a = f.pack_a ? f.pack_a : a;
+    p.b = f.pack_w ? f.pack_w : w;
+    if (moe::launch_linear_pack(packed(a, lda, M, K, f.pack_a), packed(w, ldw, N, K, f.pack_w), s) !=
+        hipSuccess)
+        return MOE_ERR_HIP;
     moe::LinearEpilogue& e = p.epi;
     e.bias = bias;
     e.residual = residual;
@@ -839,24 +839,14 @@ int32_t moe_linear_backward(const void* grad_out, int64_t ldg, int32_t grad_dtyp
     }
     const uint16_t* dz = f.need_dz ? f.dz.dz : (const uint16_t*)grad_out;
     const bool want_a = grad_a && M > 0, want_w = grad_w && N > 0;
-    if (want_a) {
-        f.da.a = dz;
-        f.da.b = w;
-        if (f.pack_w) {
-            if (moe::launch_linear_pack(w, ldw, N, K, f.pack_w, s) != hipSuccess) return MOE_ERR_HIP;
-            f.da.b = f.pack_w;
-        }
-        grad_out_epilogue(f.da.epi, grad_a, K);
-    }
-    if (want_w) {
-        f.dw.a = dz;
-        f.dw.b = a;
-        if (f.pack_a) {
-            if (moe::launch_linear_pack(a, lda, M, K, f.pack_a, s) != hipSuccess) return MOE_ERR_HIP;
-            f.dw.b = f.pack_a;
-        }
-        grad_out_epilogue(f.dw.epi, grad_w, K);
-    }
+    if (moe::launch_linear_pack(packed(w, ldw, N, K, want_a ? f.pack_w : nullptr),
+                                packed(a, lda, M, K, want_w ? f.pack_a : nullptr), s) != hipSuccess)
+        return MOE_ERR_HIP;
+    f.da.a = f.dw.a = dz;
+    f.da.b = f.pack_w ? f.pack_w : w;
+    f.dw.b = f.pack_a ? f.pack_a : a;
+    grad_out_epilogue(f.da.epi, grad_a, K);
+    grad_out_epilogue(f.dw.epi, grad_w, K);
     if (want_a && want_w && moe::linear_pair(f.da, f.dw))
         return hip_status(moe::launch_linear_pair(f.da, f.dw, dtype, s));
     if (want_a && moe::launch_linear_product(f.da, dtype, s) != hipSuccess) return MOE_ERR_HIP;

@@ -159,6 +159,13 @@ struct LinearProduct {       // C[i, j] = sum over parts and r < red of A[i, r] 
     double us;               // what the plan expects
 };
 
+struct LinearPack {          // a matrix copied into rows of cols8 (rows 0: none)
+    const uint16_t* src;
+    int64_t ld;
+    int rows, cols, cols8;
+    uint16_t* dst;
+};
+
 struct LinearDz {
     const void* grad;        // [M, N], 16-bit or fp32
     int64_t ldg;
@@ -171,6 +178,7 @@ struct LinearDz {
     float* sums;             // [linear_dz_blocks(M, N), N] or NULL
     int vec;                 // rows of grad and preact start on 16 bytes
     int lc;                  // log2 of a block's threads across the columns (set by the launch)
+    uint16_t* bias;          // grad_bias where one block sums all rows, else NULL (set by the launch)
 };
 
 // Chooses tile, split and the partial layout from the sizes (host-only, deterministic).
@@ -181,8 +189,7 @@ hipError_t launch_linear_product(const LinearProduct& p, int dtype, hipStream_t 
 bool linear_pair(LinearProduct& da, LinearProduct& dw);
 hipError_t launch_linear_pair(const LinearProduct& da, const LinearProduct& dw, int dtype,
                               hipStream_t stream);
-hipError_t launch_linear_pack(const uint16_t* src, int64_t ld, int rows, int cols, uint16_t* dst,
-                              hipStream_t stream);
+hipError_t launch_linear_pack(const LinearPack& a, const LinearPack& b, hipStream_t stream);
 int linear_dz_blocks(int M, int N);
 hipError_t launch_linear_dz(const LinearDz& p, int dtype, uint16_t* grad_bias, hipStream_t stream);
 

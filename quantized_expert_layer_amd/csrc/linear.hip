@@ -427,18 +427,32 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(LinearProduct p) {
 #endif
 }
 
-// Copies a 16-bit matrix whose rows cannot be read in 16-byte pieces (row length or stride not a
-// multiple of 8) into rows of cols8 = cols rounded up to 8, zeros behind.
-__global__ __launch_bounds__(256) void linear_pack_kernel(const uint16_t* __restrict__ src,
-                                                          int64_t ld, int rows, int cols,
-                                                          int cols8, uint16_t* __restrict__ dst) {
-    const int64_t total = (int64_t)rows * (cols8 / 2);
-    for (int64_t i = blockIdx.x * 256 + (int64_t)threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / (cols8 / 2);
-        const int c = (int)(i - r * (cols8 / 2)) * 2;
-        const uint16_t* s = src + r * ld + c;
-        const uint32_t lo = c < cols ? s[0] : 0, hi = c + 1 < cols ? s[1] : 0;
-        ((uint32_t*)dst)[i] = lo | hi << 16;
+// Copies up to two 16-bit matrices whose rows cannot be read in 16-byte pieces in place (row length or
+// stride not a multiple of 8) into rows of cols8 = cols rounded up to 8, zeros behind; eight values
+// per thread.
+__global__ __launch_bounds__(256) void linear_pack_kernel(LinearPack a, LinearPack b) {
+    struct __attribute__((packed, aligned(2))) Piece { uint32_t v[4]; };   // 16 bytes on 2
+    const int64_t na = (int64_t)a.rows * (a.cols8 / 8), nb = (int64_t)b.rows * (b.cols8 / 8);
+    for (int64_t j = blockIdx.x * 256 + (int64_t)threadIdx.x; j < na + nb; j += (int64_t)gridDim.x * 256) {
+        const LinearPack& m = j < na ? a : b;
+        const int64_t i = j < na ? j : j - na;
+        const int64_t r = i / (m.cols8 / 8);
+        const int c = (int)(i - r * (m.cols8 / 8)) * 8;
+        const uint16_t* s = m.src + r * m.ld + c;
+        u32x4 o;
+        if (c + 8 <= m.cols) {
+            const Piece q = *(const Piece*)s;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) o[h] = q.v[h];
+        } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                const uint32_t lo = c + 2 * h < m.cols ? s[2 * h] : 0;
+                const uint32_t hi = c + 2 * h + 1 < m.cols ? s[2 * h + 1] : 0;
+                o[h] = lo | hi << 16;
+            }
+        }
+        ((u32x4*)m.dst)[i] = o;
     }
 }
 
@@ -531,7 +545,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearDz p) {
         else if (p.act == MOE_ACT_GELU) dz_rows<DT, MOE_ACT_GELU>(p, col, row, step, sum);
         else dz_rows<DT, MOE_ACT_NONE>(p, col, row, step, sum);
     }
-    if (!p.sums) return;
+    if (!p.sums && !p.bias) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) red[threadIdx.x][i] = sum[i];
     __syncthreads();
@@ -539,7 +553,9 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearDz p) {
         float t = 0.0f;
         for (int r = 0; r < down; ++r) t += red[(r << p.lc) + (c >> 3)][c & 7];
         const int n = blockIdx.x * across * 8 + c;
-        if (n < p.N) p.sums[(int64_t)blockIdx.y * p.N + n] = t;
+        if (n >= p.N) continue;
+        if (p.bias) p.bias[n] = f32_to_dt<DT>(t);                  // one block down the rows
+        else p.sums[(int64_t)blockIdx.y * p.N + n] = t;
     }
 }
 
@@ -736,11 +752,10 @@ hipError_t launch_linear_pair(const LinearProduct& da, const LinearProduct& dw, 
     return hipGetLastError();
 }
 
-hipError_t launch_linear_pack(const uint16_t* src, int64_t ld, int rows, int cols, uint16_t* dst,
-                              hipStream_t s) {
-    const int cols8 = (cols + 7) / 8 * 8;
-    linear_pack_kernel<<<grid_for((int64_t)rows * (cols8 / 2), 256), 256, 0, s>>>(src, ld, rows, cols,
-                                                                              cols8, dst);
+hipError_t launch_linear_pack(const LinearPack& a, const LinearPack& b, hipStream_t s) {
+    const int64_t n = (int64_t)a.rows * (a.cols8 / 8) + (int64_t)b.rows * (b.cols8 / 8);
+    if (n == 0) return hipSuccess;
+    linear_pack_kernel<<<grid_for(n, 256), 256, 0, s>>>(a, b);
     return hipGetLastError();
 }
 
@@ -757,22 +772,24 @@ int linear_dz_blocks(int M, int N) {
     const int64_t rows = ((int64_t)M + down - 1) / down;
     int64_t want = (2048 + wide - 1) / (wide < 1 ? 1 : wide);
     if (want > 256) want = 256;
-    return (int)(rows < 1 ? 1 : rows < want ? rows : want);
+    // few rows per thread: one block, which writes the bias gradient itself (a launch less)
+    return (int)(rows <= 4 ? 1 : rows < want ? rows : want);
 }
 
 hipError_t launch_linear_dz(const LinearDz& args, int dtype, uint16_t* grad_bias, hipStream_t s) {
     LinearDz p = args;
     p.lc = dz_across(p.N);
     const int blocks = linear_dz_blocks(p.M, p.N);
+    p.bias = blocks == 1 ? grad_bias : nullptr;
     const dim3 grid((p.cols8 / 8 + (1 << p.lc) - 1) >> p.lc, blocks);
-    const int bgrid = (p.N + 63) / 64;
-    if (dtype == MOE_DT_BF16) {
-        linear_dz_kernel<MOE_DT_BF16><<<grid, 256, 0, s>>>(p);
-        if (grad_bias) linear_bias_kernel<MOE_DT_BF16><<<bgrid, 1024, 0, s>>>(p.sums, blocks, p.N, grad_bias);
-    } else {
-        linear_dz_kernel<MOE_DT_FP16><<<grid, 256, 0, s>>>(p);
-        if (grad_bias) linear_bias_kernel<MOE_DT_FP16><<<bgrid, 1024, 0, s>>>(p.sums, blocks, p.N, grad_bias);
-    }
+    auto go = [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        linear_dz_kernel<DT><<<grid, 256, 0, s>>>(p);
+        if (grad_bias && blocks > 1)
+            linear_bias_kernel<DT><<<(p.N + 63) / 64, 1024, 0, s>>>(p.sums, blocks, p.N, grad_bias);
+    };
+    if (dtype == MOE_DT_BF16) go(std::integral_constant<int, MOE_DT_BF16>{});
+    else go(std::integral_constant<int, MOE_DT_FP16>{});
     return hipGetLastError();
 }
 
