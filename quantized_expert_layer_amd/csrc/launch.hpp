@@ -212,6 +212,7 @@ struct BalanceParams {
     int32_t* part_tokens;    // [pieces]
     float* terms;            // [S]
     int vec;                 // rows of logits in 16-byte pieces (set by the launch)
+    int count_in;            // the segment that is done last writes the loss (set by the launch)
 };
 size_t balance_workspace_layout(int T, int E, int S, BalanceParams* p, char* base);
 hipError_t launch_balance(const BalanceParams& p, hipStream_t stream);

@@ -187,9 +187,30 @@ __device__ __forceinline__ T block_sum(T v, T* scratch) {
     return r;
 }
 
+// The loss from the segments' terms, in one fixed order (`load` reads them; result in thread 0).
+template <typename F, typename G>
+__device__ __forceinline__ void balance_total(const BalanceParams& p, F load_term, G load_tokens,
+                                              float* fs, int* is) {
+    float total = 0.0f;
+    int used = 0;
+    for (int i = threadIdx.x; i < p.S; i += blockDim.x) {
+        total += load_term(i);
+        used += load_tokens(i) > 0;
+    }
+    total = block_sum(total, fs);
+    used = block_sum(used, is);
+    if (threadIdx.x == 0) *p.loss = used ? p.coef * (total / (float)used) : 0.0f;
+}
+__global__ __launch_bounds__(1024) void balance_total_kernel(BalanceParams p) {
+    __shared__ float fs[16];
+    __shared__ int is[16];
+    balance_total(p, [&](int i) { return p.terms[i]; }, [&](int i) { return p.tokens[i]; }, fs, is);
+}
+
 // One segment per block: adds its pieces (group g of threads takes pieces g, g + groups, ...; the
 // groups are then added in order), writes counts, probs and tokens, and leaves the segment's term.
-// The block that arrives last adds the terms in segment order.
+// The block that arrives last adds the terms in segment order; with many segments a launch of its
+// own does (the arrivals, one after the other at one address, would take 14 ns each).
 __global__ __launch_bounds__(1024) void balance_segment_kernel(BalanceParams p) {
     __shared__ float fsum[1024];
     __shared__ int isum[1024];
@@ -235,9 +256,10 @@ __global__ __launch_bounds__(1024) void balance_segment_kernel(BalanceParams p) 
     term = block_sum(term, fs);
     if (tid == 0) {
         term = n ? term * ((float)p.E / ((float)p.k * (float)n)) : 0.0f;
-        if (p.S == 1) {
+        if (!p.count_in) {
             p.tokens[s] = n;
-            *p.loss = p.coef * term;
+            if (p.S == 1) *p.loss = p.coef * term;
+            else p.terms[s] = term;
         } else {
             // What the last block reads is written through to memory, and has been before this
             // block counts itself: the wait stands in for a release of the whole L2.
@@ -248,30 +270,35 @@ __global__ __launch_bounds__(1024) void balance_segment_kernel(BalanceParams p) 
                                           __HIP_MEMORY_SCOPE_AGENT) == p.S - 1;
         }
     }
-    if (p.S == 1) return;
+    if (!p.count_in) return;
     __syncthreads();
     if (!last) return;
-    float total = 0.0f;
-    int used = 0;
-    for (int i = tid; i < p.S; i += threads) {
-        total += __hip_atomic_load(&p.terms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        used += __hip_atomic_load(&p.tokens[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > 0;
-    }
-    total = block_sum(total, fs);
-    used = block_sum(used, is);
-    if (tid == 0) *p.loss = used ? p.coef * (total / (float)used) : 0.0f;
+    balance_total(
+        p, [&](int i) { return __hip_atomic_load(&p.terms[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); },
+        [&](int i) { return __hip_atomic_load(&p.tokens[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); },
+        fs, is);
 }
 
 // Gradient of the logits, four consecutive tokens per wave.  All rows, choices and offsets are asked
 // for before the first is used.  Bound by its arithmetic (about 250 instructions per wave): 65536 x
 // 64, 38 MB, 12.2 us with both terms (a copy of 17 MB alone takes 4.6 us); waves of 2, 4 and 8 groups
 // with the next group's loads in flight took 14.6, 15.6 and 20 us.
-template <int PER_LANE, bool GATE, bool BALANCE>
+template <int PER_LANE, bool GATE, bool BALANCE, bool MANY>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradParams p) {
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int j16 = lane & 15, row = lane >> 4;
     int used = 1;
-    if (BALANCE && p.S > 1) {                     // segments with tokens
+    if constexpr (BALANCE && MANY) {              // segments with tokens, counted by the block
+        __shared__ int share[4];
+        int n = 0;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < p.S; i += 256) n += p.tokens[i] > 0;
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o);
+        if (lane == 0) share[wave] = n;
+        __syncthreads();
+        used = max(share[0] + share[1] + share[2] + share[3], 1);
+    } else if (BALANCE && p.S > 1) {
         used = 0;
         for (int i = 0; i < p.S; i += kWave)
             used += __popcll(__ballot(i + lane < p.S && p.tokens[i + lane] > 0));
@@ -402,11 +429,12 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradParams p) 
             if (j16 * PER_LANE + i < p.E) dst[i] = g[i];
     };
 
-    const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * 4;
-    if (first >= p.T) return;
-    Group g;
-    fetch((int)first, g);
-    compute((int)first, g);
+    for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 4; t0 < p.T; t0 += (int64_t)gridDim.x * 16) {
+        Group g;
+        fetch((int)t0, g);
+        compute((int)t0, g);
+        if (!MANY) return;
+    }
 }
 
 // Gradients of the combine, one token per block: each thread takes 8 columns at a time, reads the
@@ -517,6 +545,8 @@ static bool in_pieces(int E, const void* a, const void* b) {
     return E % 4 == 0 && (((uintptr_t)a | (uintptr_t)b) & 15) == 0;
 }
 
+constexpr int kTotalLaunch = 128;
+
 hipError_t launch_balance(const BalanceParams& args, hipStream_t s) {
     BalanceParams p = args;
     p.vec = in_pieces(p.E, p.logits, nullptr);
@@ -524,20 +554,34 @@ hipError_t launch_balance(const BalanceParams& args, hipStream_t s) {
     else if (p.E <= 64) balance_piece_kernel<4><<<p.pieces, 256, 0, s>>>(p);
     else if (p.E <= 128) balance_piece_kernel<8><<<p.pieces, 256, 0, s>>>(p);
     else balance_piece_kernel<16><<<p.pieces, 256, 0, s>>>(p);
+    const bool launch_total = p.S > kTotalLaunch;
+    p.count_in = p.S > 1 && !launch_total;
     balance_segment_kernel<<<p.S, p.pieces / p.S > 64 ? 1024 : 256, 0, s>>>(p);
+    if (launch_total) balance_total_kernel<<<1, 1024, 0, s>>>(p);
     return hipGetLastError();
 }
 
 hipError_t launch_route_backward(const RouteGradParams& args, hipStream_t s) {
     RouteGradParams p = args;
     p.vec = in_pieces(p.E, p.logits, p.grad) && ((uintptr_t)p.counts & 15) == 0;
-    const int grid = (int)(((int64_t)p.T + 15) / 16);
+    // Every wave counts the segments that have tokens.  From some hundred on (512: 18.7 us either way)
+    // the block does, and from 2048 blocks on the blocks take several groups of tokens each: 65536 x
+    // 64 of 4096 segments 22.6 against 41.3 us, of 65536 segments 52 against 412.
+    const bool many = p.counts && p.S > 512;
+    int grid = (int)(((int64_t)p.T + 15) / 16);
+    if (many && grid > 2048) grid = 2048;
+    auto run = [&](auto gate, auto balance, auto mn) {
+        constexpr bool G = decltype(gate)::value, B = decltype(balance)::value, M = decltype(mn)::value;
+        if (p.E <= 16) route_backward_kernel<1, G, B, M><<<grid, 256, 0, s>>>(p);
+        else if (p.E <= 64) route_backward_kernel<4, G, B, M><<<grid, 256, 0, s>>>(p);
+        else if (p.E <= 128) route_backward_kernel<8, G, B, M><<<grid, 256, 0, s>>>(p);
+        else route_backward_kernel<16, G, B, M><<<grid, 256, 0, s>>>(p);
+    };
     auto go = [&](auto gate, auto balance) {
-        constexpr bool G = decltype(gate)::value, B = decltype(balance)::value;
-        if (p.E <= 16) route_backward_kernel<1, G, B><<<grid, 256, 0, s>>>(p);
-        else if (p.E <= 64) route_backward_kernel<4, G, B><<<grid, 256, 0, s>>>(p);
-        else if (p.E <= 128) route_backward_kernel<8, G, B><<<grid, 256, 0, s>>>(p);
-        else route_backward_kernel<16, G, B><<<grid, 256, 0, s>>>(p);
+        if constexpr (decltype(balance)::value) {
+            if (many) return run(gate, balance, std::true_type{});
+        }
+        run(gate, balance, std::false_type{});
     };
     if (p.grad_w && p.counts) go(std::true_type{}, std::true_type{});
     else if (p.grad_w) go(std::true_type{}, std::false_type{});

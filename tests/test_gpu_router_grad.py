@@ -132,6 +132,32 @@ def test_balance_packed_batch():
     _check_balance(9000, 64, 6, [0] + cuts + [9000], True, seed=1, what="S=300")
 
 
+@pytest.mark.parametrize("T,E,k,S", [(40000, 16, 2, 600), (300, 24, 2, 5000), (40000, 60, 4, 5000),
+                                     (3000, 130, 3, 129), (3000, 200, 3, 1025)])
+def test_balance_many_segments(T, E, k, S):
+    """Counts of segments beyond what a wave, a block and one launch deal with, and both terms of the
+    gradient in one pass over them."""
+    import torch
+    cuts = np.sort(np.random.default_rng(S).integers(0, T + 1, S - 1)).tolist()
+    offsets = [0] + cuts + [T]
+    _check_balance(T, E, k, offsets, True, seed=S, what=f"S={S}")
+    logits, ids, active = _inputs(T, E, k, 1)
+    g = torch.Generator(device="cuda").manual_seed(S)
+    w, gw = (torch.rand((T, k), generator=g, device="cuda") for _ in range(2))
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    _, counts, _, tokens = q.moe_balance_loss(logits, ids, 1.0, active=active, seq_offsets=off)
+    part = dict(counts=counts, tokens=tokens, coef=1.0, seq_offsets=off)
+    for mode in ("topk", "all"):
+        gate = dict(gate_mode=mode, topk_w=w, grad_w=gw)
+        both = q.moe_route_backward(logits, ids, active=active, **gate, **part)
+        a = q.moe_route_backward(logits, ids, active=active, **gate)
+        b = q.moe_route_backward(logits, ids, active=active, **part)
+        # "all" adds a slot's term and the row's: three roundings of no more than the terms' sum,
+        # which is below k + 1 here
+        tol = 2 * U * (a.abs() + b.abs()) if mode == "topk" else 3 * U * (b.abs() + 2 * (k + 1))
+        assert ((both - (a + b)).abs() <= tol).all()
+
+
 def test_balance_all_padding_masked_rows_and_empty_batch():
     import torch
     logits, ids, _ = _inputs(20, 12, 2, 0)
@@ -381,6 +407,18 @@ def test_router_tuning_step(name, T):
     with pytest.raises(ValueError):                  # a layer that only makes the decode call
         only = q.DeviceLayer.from_inputs(inp, decode=True)
         only.router_backward(out, lg, ws)
+    # a workspace that holds no unscaled expert rows: none yet, or of a forward() or a plan with the
+    # gate weight in the GEMM
+    fresh = layer.workspace(T)
+    with pytest.raises(ValueError):
+        layer.router_backward(out, lg, fresh)
+    for fill in (lambda: layer.forward(x, lg, ws=fresh), lambda: layer.plan(fresh, x, lg)):
+        layer.forward(x, lg, ws=fresh, gate_in_gemm=False)
+        layer.router_backward(out, lg, fresh)
+        fill()
+        with pytest.raises(ValueError):
+            layer.router_backward(out, lg, fresh)
+    torch.cuda.synchronize()
 
 
 def test_router_offsets_past_32_bits():
