@@ -478,10 +478,11 @@ size_t moe_linear_workspace_size(int32_t M, int32_t N, int32_t K, int64_t lda, i
  *   ws         at least moe_linear_backward_workspace_size(...) bytes, as for moe_linear
  *   Sums are fp32.  grad_bias sums the unrounded dz.  The products read dz in dtype: a 16-bit
  *   gradient with MOE_ACT_NONE or RELU is exact there; an fp32 gradient enters as two 16-bit parts
- *   (its first 16 bits in bf16, 22 in fp16), and so does one through SILU or GELU with M < 256,
- *   which is rounded once to dtype with more rows.
+ *   (its first 16 bits in bf16, 22 in fp16, there to no finer than 2^-25), and so does one through
+ *   SILU or GELU with M < 256, which is rounded once to dtype with more rows.
  *   fp16 has a short range: scale the loss so that dz lies within it, as fp16 training does.
- *   With M == 0 grad_w and grad_bias, and with N == 0 grad_a, are written as zeros.
+ *   With M == 0 grad_w and grad_bias, and with N == 0 grad_a, are written as zeros.  No output may
+ *   overlap an input.
  * Errors: as moe_linear, plus MOE_ERR_INVALID when no gradient is wanted, or for an activation
  * without preact.
  */
@@ -510,7 +511,8 @@ size_t moe_linear_backward_workspace_size(int32_t M, int32_t N, int32_t K, int64
  *   seq_offsets  int32 [S + 1] or NULL (then S must be 1: all T tokens): segment s holds tokens
  *                seq_offsets[s] .. seq_offsets[s+1] - 1; non-decreasing values in [0, T].  Empty
  *                segments are allowed; tokens before the first or behind the last belong to none.
- *                (Values outside are clamped, a decreasing pair is an empty segment.)
+ *                (Values outside are clamped.  Of offsets that decrease nothing out of range is read
+ *                or written, but the results mean nothing.)
  *   loss         fp32 [1] out: 0 when no token is live
  *   counts       int32 [S, E] out;  probs fp32 [S, E] out (0 for an empty segment);
  *   tokens       int32 [S] out: n_s
@@ -541,7 +543,8 @@ size_t moe_balance_workspace_size(int32_t T, int32_t E, int32_t S);
  *                with an id outside [0, E) are left out
  *   counts, tokens  what moe_balance_loss wrote, both or neither NULL
  *   grad_loss    fp32 [1] on the device, or NULL (= 1)
- *   grad_logits  fp32 [T, E] out: every element is written (a token that is not live gets zeros)
+ *   grad_logits  fp32 [T, E] out: every element is written (a token that is not live gets zeros);
+ *                overlaps no input
  * Errors: MOE_ERR_INVALID when neither grad_w nor counts is given, or for grad_w without topk_w.
  */
 int32_t moe_route_backward(const float* logits, const int32_t* topk_ids, const float* topk_w,
@@ -561,7 +564,8 @@ int32_t moe_route_backward(const float* logits, const int32_t* topk_ids, const f
  *   y_perm    fp16 [R, d], R >= T*k rows; read for grad_w only
  *   topk_w    fp32 [T, k]; read for grad_y only
  *   grad_w    fp32 [T, k] out, or NULL: not wanted; a dropped slot (inv_perm outside [0, T*k)) gets 0
- *   grad_y    fp16 [R, d] out, or NULL; rows no slot points at are left as they were
+ *   grad_y    fp16 [R, d] out, or NULL; rows no slot points at are left as they were; may not overlap
+ *             an input
  *   Sums are fp32.  Requires 1 <= k <= 8, d % 8 == 0, T < 2^24, and grad_w or grad_y.
  */
 int32_t moe_combine_backward(const uint16_t* grad_out, const uint16_t* y_perm,

@@ -612,6 +612,12 @@ def _here(dev):
     return _torch().cuda.current_stream(dev).cuda_stream if raw is None else raw(dev.index)
 
 
+def _sizes(*sizes):
+    """Refuses what the C entry points' 32-bit sizes would cut off."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"sizes must be below 2^31, got {sizes}")
+
+
 def _refuse(t, dtype, name, shape, dev):
     """Raises for the first thing that is wrong with t's type, device or shape."""
     if not isinstance(t, _torch().Tensor):
@@ -697,6 +703,7 @@ def moe_linear(a, w, bias=None, act="none", residual=None, out=None, out_dtype=N
         raise ValueError("a and w must have two dimensions")
     M, K = a.shape
     N = w.shape[0]
+    _sizes(M, N, K)
     dev, dtype = a.device, a.dtype
     dt = _dt(dtype, "a")
     with _place(a, stream):
@@ -737,6 +744,7 @@ def moe_linear_backward(grad_out, a, w, act="none", preact=None, need_a=True, ne
         raise ValueError("a and w must have two dimensions")
     M, K = a.shape
     N = w.shape[0]
+    _sizes(M, N, K)
     dev, dtype = a.device, a.dtype
     dt = _dt(dtype, "a")
     ac = _linear_act(act)
@@ -774,6 +782,7 @@ def _segments(seq_offsets, dev):
     if seq_offsets is None:
         return 1, None
     S = seq_offsets.numel() - 1
+    _sizes(S)
     ps = _dense(seq_offsets, _torch().int32, "seq_offsets", (S + 1,), dev)
     if S < 1:
         raise ValueError("seq_offsets needs at least two entries")
@@ -787,6 +796,7 @@ def moe_balance_loss(logits, topk_ids, coef, active=None, seq_offsets=None, loss
     torch = _torch()
     T, E = logits.shape
     k = topk_ids.shape[1]
+    _sizes(T, E, k)
     dev = logits.device
     with _place(logits, stream):
         S, ps = _segments(seq_offsets, dev)
@@ -822,6 +832,7 @@ def moe_route_backward(logits, topk_ids, gate_mode="topk", topk_w=None, grad_w=N
     torch = _torch()
     T, E = logits.shape
     k = topk_ids.shape[1]
+    _sizes(T, E, k)
     dev = logits.device
     with _place(logits, stream):
         S, ps = _segments(seq_offsets, dev)
@@ -851,6 +862,7 @@ def moe_combine_backward(grad_out, y_perm, inv_perm, topk_w, need_w=True, need_y
     T, d = grad_out.shape
     k = topk_w.shape[1]
     R = y_perm.shape[0]
+    _sizes(T, d, k)
     dev = grad_out.device
     with _place(grad_out, stream):
         if grad_w is None and need_w:

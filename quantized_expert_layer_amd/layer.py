@@ -36,6 +36,7 @@ class Workspace:
     """Per-(T) device buffers reused across forward() calls."""
     T: int
     bufs: Dict[str, object] = field(default_factory=dict)
+    rows_unscaled: bool = False          # "y" holds expert rows without their gate weight
 
 
 class DeviceLayer:
@@ -184,6 +185,7 @@ class DeviceLayer:
             ws = self.workspace(T)
         b = ws.bufs
         path = self.gemm_path
+        ws.rows_unscaled = not gate_in_gemm
         if self.uses_decode(T, gate_in_gemm):
             if self._shared_in_decode():
                 moe_decode_layer_shared(logits, x, self.k, self.gate_mode, self.inter, self.act,
@@ -265,6 +267,9 @@ class DeviceLayer:
         T = ws.T
         if self.uses_decode(T, gate_in_gemm=False):
             raise ValueError("the decode call keeps no expert rows: use decode=None or False")
+        if not ws.rows_unscaled:
+            raise ValueError("ws holds no unscaled expert rows: call forward() with "
+                             "gate_in_gemm=False first")
         if grad_out.shape != (T, self.d) or logits.shape != (T, self.E):
             raise ValueError(f"expected grad_out {(T, self.d)} and logits {(T, self.E)}, got "
                              f"{tuple(grad_out.shape)} and {tuple(logits.shape)}")
@@ -289,6 +294,7 @@ class DeviceLayer:
         w1, w2 = weights[:2] if weights is not None else (self.w1, self.w2)
         shw = tuple(weights[2:4]) if weights is not None and len(weights) == 4 else self.shared
         b, L, T = ws.bufs, lib(), ws.T
+        ws.rows_unscaled = not gate_in_gemm
         st = _stream(stream)
         path = self.gemm_path
         opts = None

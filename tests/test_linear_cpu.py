@@ -95,6 +95,22 @@ def test_nothing_to_do_is_accepted_without_pointers():
     assert L.moe_combine_backward(*dict(COMBINE, T=0, go=None).values()) == q.MOE_OK
 
 
+def test_sizes_past_32_bits_are_refused_and_not_cut_off():
+    import torch
+    n = (1 << 32) + 4                                  # 4 in 32 bits
+    like = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device="meta")
+    f32, i32 = torch.float32, torch.int32
+    for call in (lambda: q.moe_linear(like(n, 8), like(8, 8)),
+                 lambda: q.moe_linear(like(8, 8), like(n, 8)),
+                 lambda: q.moe_linear_backward(like(n, 8), like(n, 8), like(8, 8)),
+                 lambda: q.moe_balance_loss(like(n, 2, dtype=f32), like(n, 1, dtype=i32), 1.0),
+                 lambda: q.moe_route_backward(like(n, 2, dtype=f32), like(n, 1, dtype=i32)),
+                 lambda: q.moe_combine_backward(like(n, 8), like(n, 8), like(n, dtype=i32),
+                                                like(n, 1, dtype=f32))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+
+
 def test_workspace_sizes():
     size = q.moe_linear_workspace_size
     assert size(0, 8, 64) == 0 and size(4, 0, 64) == 0 and size(-1, 8, 64) == 0
