@@ -298,6 +298,36 @@ def test_combine_gradients(T, d, k, E):
     assert a is None and torch.equal(b, gy)
 
 
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -130])             # 2^-130: subnormal terms
+def test_gate_gradient_of_one_expert_in_every_slot(scale):
+    """Eight slots of a token that name one expert, or two: their terms add up, the same bits each time."""
+    import torch
+    T, E, k = 100, 24, 8
+    g = torch.Generator(device="cuda").manual_seed(2)
+    logits = torch.randn((T, E), generator=g, device="cuda")
+    w = torch.rand((T, k), generator=g, device="cuda") * scale
+    gw = torch.randn((T, k), generator=g, device="cuda")
+    ids = torch.full((T, k), 5, dtype=torch.int32, device="cuda")
+    ids[50:, ::3] = 19
+    case(f"gate gradient of repeated ids, scale {scale}")
+    for mode in ("topk", "all"):
+        first = q.moe_route_backward(logits, ids, gate_mode=mode, topk_w=w, grad_w=gw)
+        for _ in range(20):
+            assert torch.equal(first, q.moe_route_backward(logits, ids, gate_mode=mode, topk_w=w, grad_w=gw))
+        w64, gw64 = w.double().cpu(), gw.double().cpu()
+        u = (w64 * gw64).sum(dim=1, keepdim=True)
+        ref = torch.zeros((T, E), dtype=torch.float64)
+        # magnitude of all terms, on every expert: a slot's product, the row's sum and its share
+        mag = (w64 * gw64).abs().sum(dim=1, keepdim=True) * (1 + w64.sum(dim=1, keepdim=True)) + u.abs()
+        if mode == "topk":
+            ref.scatter_add_(1, ids.cpu().long(), w64 * (gw64 - u))
+        else:
+            ref.scatter_add_(1, ids.cpu().long(), w64 * gw64)
+            ref -= _softmax64(logits).cpu() * u
+        # about 40 roundings of at most 2^-24 of that, each of a subnormal of at most 2^-150
+        assert ((first.cpu().double() - ref).abs() <= 40 * (U * mag + 2.0 ** -150)).all(), mode
+
+
 def test_router_refusals():
     import torch
     logits, ids, active = _inputs(6, 8, 2, 0)
