@@ -608,8 +608,9 @@ def _place(ref, stream):
 def _here(dev):
     """Handle of dev's current stream (asked for without building a Stream object: that costs as
     much host time as the call itself)."""
-    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
-    return _torch().cuda.current_stream(dev).cuda_stream if raw is None else raw(dev.index)
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(dev).cuda_stream if raw is None else raw(dev.index)
 
 
 def _sizes(*sizes):
@@ -639,6 +640,14 @@ def _dense(t, dtype, name, shape, dev):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _out(t, dtype, name, shape, dev):
+    """(t, its address) of a dense output, allocated if None."""
+    if t is None:
+        t = new_output(shape, dtype, dev)
+        return t, t.data_ptr()
+    return t, _dense(t, dtype, name, shape, dev)
 
 
 def _rows(t, dtype, name, shape, dev):
@@ -709,13 +718,15 @@ def moe_linear(a, w, bias=None, act="none", residual=None, out=None, out_dtype=N
     with _place(a, stream):
         if out is None:
             out = new_output((M, N), out_dtype or dtype, dev)
+            po, ldo = out.data_ptr(), N
         elif out_dtype is not None and out.dtype != out_dtype:
             raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
+        else:
+            po, ldo = _rows(out, out.dtype, "out", (M, N), dev)
         od = DT_FP32 if out.dtype == torch.float32 else _dt(out.dtype, "out")
         pa, lda = _rows(a, dtype, "a", (M, K), dev)
         pw, ldw = _rows(w, dtype, "w", (N, K), dev)
         pr, ldr = _rows(residual, dtype, "residual", (M, N), dev)
-        po, ldo = _rows(out, out.dtype, "out", (M, N), dev)
         pp, ldp = _rows(preact, dtype, "preact", (M, N), dev)
         pb = _dense(bias, dtype, "bias", (N,), dev)
         ac = _linear_act(act)
@@ -749,21 +760,19 @@ def moe_linear_backward(grad_out, a, w, act="none", preact=None, need_a=True, ne
     dt = _dt(dtype, "a")
     ac = _linear_act(act)
     with _place(a, stream):
-        if grad_a is None and need_a:
-            grad_a = new_output((M, K), dtype, dev)
-        if grad_w is None and need_w:
-            grad_w = new_output((N, K), dtype, dev)
-        if grad_bias is None and need_bias:
-            grad_bias = new_output((N,), dtype, dev)
+        pga = pgw = pgb = None
+        if grad_a is not None or need_a:
+            grad_a, pga = _out(grad_a, dtype, "grad_a", (M, K), dev)
+        if grad_w is not None or need_w:
+            grad_w, pgw = _out(grad_w, dtype, "grad_w", (N, K), dev)
+        if grad_bias is not None or need_bias:
+            grad_bias, pgb = _out(grad_bias, dtype, "grad_bias", (N,), dev)
         gd = grad_out.dtype
         gdt = DT_FP32 if gd == torch.float32 else _dt(gd, "grad_out")
         pg, ldg = _rows(grad_out, gd, "grad_out", (M, N), dev)
         pa, lda = _rows(a, dtype, "a", (M, K), dev)
         pw, ldw = _rows(w, dtype, "w", (N, K), dev)
         pp, ldp = _rows(preact, dtype, "preact", (M, N), dev)
-        pga = _dense(grad_a, dtype, "grad_a", (M, K), dev)
-        pgw = _dense(grad_w, dtype, "grad_w", (N, K), dev)
-        pgb = _dense(grad_bias, dtype, "grad_bias", (N,), dev)
         L = lib()
         need = L.moe_linear_backward_workspace_size(M, N, K, lda, ldw, ldg, gdt, ac)
         ws, pws, nws = _workspace(need, ws, dev)
@@ -800,22 +809,14 @@ def moe_balance_loss(logits, topk_ids, coef, active=None, seq_offsets=None, loss
     dev = logits.device
     with _place(logits, stream):
         S, ps = _segments(seq_offsets, dev)
-        if loss is None:
-            loss = new_output((1,), torch.float32, dev)
-        if counts is None:
-            counts = new_output((S, E), torch.int32, dev)
-        if probs is None:
-            probs = new_output((S, E), torch.float32, dev)
-        if tokens is None:
-            tokens = new_output((S,), torch.int32, dev)
         f32, i32 = torch.float32, torch.int32
+        loss, po = _out(loss, f32, "loss", (1,), dev)
+        counts, pc = _out(counts, i32, "counts", (S, E), dev)
+        probs, pp = _out(probs, f32, "probs", (S, E), dev)
+        tokens, pt = _out(tokens, i32, "tokens", (S,), dev)
         pl = _dense(logits, f32, "logits", (T, E), dev)
         pi = _dense(topk_ids, i32, "topk_ids", (T, k), dev)
         pa = _dense(active, torch.uint8, "active", (T,), dev)
-        po = _dense(loss, f32, "loss", (1,), dev)
-        pc = _dense(counts, i32, "counts", (S, E), dev)
-        pp = _dense(probs, f32, "probs", (S, E), dev)
-        pt = _dense(tokens, i32, "tokens", (S,), dev)
         L = lib()
         ws, pws, nws = _workspace(L.moe_balance_workspace_size(T, E, S), ws, dev)
         _check("moe_balance_loss", L.moe_balance_loss(
@@ -836,9 +837,8 @@ def moe_route_backward(logits, topk_ids, gate_mode="topk", topk_w=None, grad_w=N
     dev = logits.device
     with _place(logits, stream):
         S, ps = _segments(seq_offsets, dev)
-        if grad_logits is None:
-            grad_logits = new_output((T, E), torch.float32, dev)
         f32, i32 = torch.float32, torch.int32
+        grad_logits, po = _out(grad_logits, f32, "grad_logits", (T, E), dev)
         pl = _dense(logits, f32, "logits", (T, E), dev)
         pi = _dense(topk_ids, i32, "topk_ids", (T, k), dev)
         pw = _dense(topk_w, f32, "topk_w", (T, k), dev)
@@ -847,7 +847,6 @@ def moe_route_backward(logits, topk_ids, gate_mode="topk", topk_w=None, grad_w=N
         pc = _dense(counts, i32, "counts", (S, E), dev)
         pt = _dense(tokens, i32, "tokens", (S,), dev)
         pgl = _dense(grad_loss, f32, "grad_loss", (1,), dev)
-        po = _dense(grad_logits, f32, "grad_logits", (T, E), dev)
         _check("moe_route_backward", lib().moe_route_backward(
             pl, pi, pw, pg, pa, ps, S, T, E, k, GATES.get(gate_mode, gate_mode), pc, pt,
             float(coef), pgl, po, _here(dev)))
@@ -865,18 +864,17 @@ def moe_combine_backward(grad_out, y_perm, inv_perm, topk_w, need_w=True, need_y
     _sizes(T, d, k)
     dev = grad_out.device
     with _place(grad_out, stream):
-        if grad_w is None and need_w:
-            grad_w = new_output((T, k), torch.float32, dev)
-        if grad_y is None and need_y:
-            grad_y = new_output((R, d), torch.float16, dev)
+        pgw = pgy = None
+        if grad_w is not None or need_w:
+            grad_w, pgw = _out(grad_w, torch.float32, "grad_w", (T, k), dev)
+        if grad_y is not None or need_y:
+            grad_y, pgy = _out(grad_y, torch.float16, "grad_y", (R, d), dev)
         pg = _dense(grad_out, torch.float16, "grad_out", (T, d), dev)
         py = _dense(y_perm, torch.float16, "y_perm", (R, d), dev)
         if R < T * k:
             raise ValueError(f"y_perm: needs at least {T * k} rows, has {R}")
         pi = _dense(inv_perm, torch.int32, "inv_perm", (T * k,), dev)
         pw = _dense(topk_w, torch.float32, "topk_w", (T, k), dev)
-        pgw = _dense(grad_w, torch.float32, "grad_w", (T, k), dev)
-        pgy = _dense(grad_y, torch.float16, "grad_y", (R, d), dev)
         _check("moe_combine_backward", lib().moe_combine_backward(
             pg, py, pi, pw, T, k, d, pgw, pgy, _here(dev)))
     return grad_w, grad_y
