@@ -662,6 +662,8 @@ struct LinearBackward {
     moe::LinearDz dz;
     uint16_t *pack_a, *pack_w;
     bool need_dz;             // the products read a copy of the gradient
+    bool narrow;              // both gradients in one pass, where both are wanted
+    float* part;
 };
 
 LinearBackward linear_backward(int32_t M, int32_t N, int32_t K, int64_t lda, int64_t ldw, int64_t ldg,
@@ -712,9 +714,12 @@ LinearBackward linear_backward(int32_t M, int32_t N, int32_t K, int64_t lda, int
     f.dw.a_part = (int64_t)M * N8;
     moe::linear_plan(f.dw);
     const size_t pa = moe::linear_part_bytes(f.da), pw = moe::linear_part_bytes(f.dw);
-    float* part = (float*)c.take(pa > pw ? pa : pw);       // the products run one after the other
-    f.da.part = f.da.split > 1 ? part : nullptr;
-    f.dw.part = f.dw.split > 1 ? part : nullptr;
+    const size_t pn = moe::linear_narrow_bytes(f.da, f.dw);
+    const size_t most = pa > pw ? pa : pw;                 // the products run one after the other
+    f.part = (float*)c.take(most > pn ? most : pn);
+    f.narrow = pn > 0;
+    f.da.part = f.da.split > 1 ? f.part : nullptr;
+    f.dw.part = f.dw.split > 1 ? f.part : nullptr;
     return f;
 }
 
@@ -847,6 +852,10 @@ int32_t moe_linear_backward(const void* grad_out, int64_t ldg, int32_t grad_dtyp
     f.dw.b = f.pack_a ? f.pack_a : a;
     grad_out_epilogue(f.da.epi, grad_a, K);
     grad_out_epilogue(f.dw.epi, grad_w, K);
+    if (want_a && want_w && f.narrow) {
+        f.dw.part = f.part;
+        return hip_status(moe::launch_linear_narrow(f.da, f.dw, dtype, s));
+    }
     if (want_a && want_w && moe::linear_pair(f.da, f.dw))
         return hip_status(moe::launch_linear_pair(f.da, f.dw, dtype, s));
     if (want_a && moe::launch_linear_product(f.da, dtype, s) != hipSuccess) return MOE_ERR_HIP;

@@ -189,6 +189,10 @@ hipError_t launch_linear_product(const LinearProduct& p, int dtype, hipStream_t 
 bool linear_pair(LinearProduct& da, LinearProduct& dw);
 hipError_t launch_linear_pair(const LinearProduct& da, const LinearProduct& dw, int dtype,
                               hipStream_t stream);
+// Both gradients of a narrow layer (its input gradient's plan is the narrow one) in one pass;
+// dw.part holds linear_narrow_bytes.
+size_t linear_narrow_bytes(const LinearProduct& da, const LinearProduct& dw);
+hipError_t launch_linear_narrow(const LinearProduct& da, LinearProduct dw, int dtype, hipStream_t stream);
 hipError_t launch_linear_pack(const LinearPack& a, const LinearPack& b, hipStream_t stream);
 int linear_dz_blocks(int M, int N);
 hipError_t launch_linear_dz(const LinearDz& p, int dtype, uint16_t* grad_bias, hipStream_t stream);

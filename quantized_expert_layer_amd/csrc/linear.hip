@@ -234,24 +234,65 @@ __global__ __launch_bounds__(512) void linear_pair_kernel(LinearProduct da, Line
 // Input gradient of a narrow layer (N <= 64, a router): da = dz w is a write of M x K with next to no
 // arithmetic.  A block holds its 256 columns of w in registers (through one LDS stage and the
 // transposing reads) and walks down `rows` rows, 16 at a time, the next rows' dz on its way.  The
-// four products of a 16 x 64 piece take columns 16 g + 4 j + i (g the lane's quarter, j the product,
-// i its result), so a lane ends up with 16 consecutive columns and a row leaves as whole lines.
-// Bound by the write: 8192 x 4096 from fp32 gradients of 16 experts, 67 MB, 22 us (30 us in tiles).
+// four products of a 16 x 64 piece take columns 32 (j / 2) + 8 g + 4 (j % 2) + i (g the lane's
+// quarter, j the product, i its result), so a lane ends up with two runs of eight columns and a row's
+// four lanes store 64 bytes in a run.  Bound by the write: 8192 x 4096 from 16-bit gradients of 16
+// experts, 67 MB, 18.7 us (20.0 us with 16 columns per lane; 30 us in tiles; a fill takes 11.8).
 // ------------------------------------------------------------------------------------
-template <int DT>
-__global__ __launch_bounds__(256) void linear_thin_kernel(LinearProduct p, int rows) {
 #ifdef __HIP_DEVICE_COMPILE__
-    using OB = Operand<256, true, 4>;
-    __shared__ __attribute__((aligned(1024))) char lds[OB::kBytes];
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int n0 = blockIdx.x * 256;
-    OB ob;
+using ThinW = Operand<256, true, 4>;                           // 256 columns of w, or of a
+// w's columns n0 .. n0 + 255 on their way to LDS, and from there as this wave's fragments of them.
+__device__ __forceinline__ void thin_load(const LinearProduct& p, int n0, uint32_t lds, int wave, int lane) {
+    ThinW ob;
     ob.init(p.b, p.ldb, n0, p.b_outs, p.b_red, wave, lane);
     const auto wb = ob.stage(ob.base, p.b_red, p.b_red > 0);
 #pragma unroll
-    for (int i = 0; i < OB::kLoads; ++i)
-        ob.load(wb, i, p.b_red, (uint32_t)(uintptr_t)(lds_void*)lds, wave);
+    for (int i = 0; i < ThinW::kLoads; ++i) ob.load(wb, i, p.b_red, lds, wave);
+}
+template <int H>
+__device__ __forceinline__ void thin_weights(const char* lds, int wave, int lane, s16x8 (&w)[H][4]) {
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = 32 * h + 8 * (lane >> 4) + ((lane >> 2) & 3);
+            const uint32_t s = (((lane >> 2) & 3) | ((lane >> 4) << 2)) & ThinW::kPairMask;
+            const char* q = lds + r * 512 +
+                (((uint32_t)(wave * 4 + 2 * (j >> 1) + ((lane >> 1) & 1)) ^ s) << 5) +
+                (lane & 1) * 16 + (j & 1) * 8;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)q);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(q + 4 * 512));
+            w[h][j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+}
+// The lane's columns of a row: eight from `col` on and eight from col + 32 on.
+template <int DT>
+__device__ __forceinline__ void thin_store(const LinearProduct& p, const f32x4 (&acc)[4], int64_t row,
+                                           int col) {
+    uint16_t* dst = (uint16_t*)p.epi.out + row * p.epi.ldo + col;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const float v[8] = {acc[2 * c][0], acc[2 * c][1], acc[2 * c][2], acc[2 * c][3],
+                            acc[2 * c + 1][0], acc[2 * c + 1][1], acc[2 * c + 1][2], acc[2 * c + 1][3]};
+        if (p.epi.vec && col + 32 * c + 8 <= p.N) {
+            *(u32x4*)(dst + 32 * c) = pack16<DT>(v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + 32 * c + i < p.N) dst[32 * c + i] = f32_to_dt<DT>(v[i]);
+        }
+    }
+}
+#endif
+
+template <int DT>
+__global__ __launch_bounds__(256) void linear_thin_kernel(LinearProduct p, int rows) {
+#ifdef __HIP_DEVICE_COMPILE__
+    __shared__ __attribute__((aligned(1024))) char lds[ThinW::kBytes];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int n0 = blockIdx.x * 256;
+    thin_load(p, n0, (uint32_t)(uintptr_t)(lds_void*)lds, wave, lane);
     // dz: row lane & 15, summed indices 8 (lane >> 4) .. + 7 of each half; past the end zeros
     const int64_t m0 = (int64_t)blockIdx.y * rows;
     const int left = (int)min((int64_t)rows, p.M - m0);
@@ -273,18 +314,8 @@ __global__ __launch_bounds__(256) void linear_thin_kernel(LinearProduct p, int r
     __builtin_amdgcn_s_waitcnt(0x0070);
     __syncthreads();
     s16x8 w[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = 32 * h + 8 * (lane >> 4) + ((lane >> 2) & 3);
-            const uint32_t s = (((lane >> 2) & 3) | ((lane >> 4) << 2)) & OB::kPairMask;
-            const char* q = lds + r * 512 + (((uint32_t)(wave * 4 + (lane & 3)) ^ s) << 5) + j * 8;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)q);
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(q + 4 * 512));
-            w[h][j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
-    const int col = n0 + wave * 64 + (lane >> 4) * 16;
+    thin_weights(lds, wave, lane, w);
+    const int col = n0 + wave * 64 + (lane >> 4) * 8;
     for (int r = 0; r < left; r += 16) {
         fetch(r + 16, nz);                                     // past the end: nothing is read
         f32x4 acc[4];
@@ -299,25 +330,147 @@ __global__ __launch_bounds__(256) void linear_thin_kernel(LinearProduct p, int r
             }
         }
         const int row = r + (lane & 15);
-        if (row < left) {
-            uint16_t* dst = (uint16_t*)p.epi.out + (m0 + row) * p.epi.ldo + col;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float v[8] = {acc[2 * c][0], acc[2 * c][1], acc[2 * c][2], acc[2 * c][3],
-                                    acc[2 * c + 1][0], acc[2 * c + 1][1], acc[2 * c + 1][2], acc[2 * c + 1][3]};
-                if (p.epi.vec && col + 8 * c + 8 <= p.N) {
-                    *(u32x4*)(dst + 8 * c) = pack16<DT>(v);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (col + 8 * c + i < p.N) dst[8 * c + i] = f32_to_dt<DT>(v[i]);
-                }
-            }
-        }
+        if (row < left) thin_store<DT>(p, acc, m0 + row, col);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) z[i][h] = nz[i][h];
+    }
+#endif
+}
+
+// Both gradients of a narrow layer in one pass over the rows: da is written and a is read at the same
+// time.  A block has 256 columns (64 a wave) and a share of the rows, 64 at a time through two
+// buffers: the stage's dz (both parts) and columns of a land in LDS, da = dz w leaves from
+// registers as in the kernel above, and dw += dz^T a stays in registers until the end, one partial sum
+// per share.  NO: N rounded up to 32 or 64.  Bound by memory: 8192 x 4096 from 16-bit gradients of 16
+// experts, 134 MB, 34 us (the two kernels one after the other 38), of which about 8 us are the first
+// loads and the last sums; a third buffer changed nothing.
+template <int DT, int NO>
+__global__ __launch_bounds__(256) void linear_narrow_kernel(LinearProduct da, LinearProduct dw) {
+#ifdef __HIP_DEVICE_COMPILE__
+    using OZ = Operand<NO, true, 4>;
+    constexpr int kStage = ThinW::kBytes + 2 * OZ::kBytes, NL = ThinW::kLoads + 2 * OZ::kLoads;
+    __shared__ __attribute__((aligned(1024))) char lds[2 * kStage];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int n0 = blockIdx.x * 256, z = blockIdx.y;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)lds;
+    auto sync = [](auto keep) {                    // all but the last `keep` stages have landed
+        constexpr int n = decltype(keep)::value * NL;
+        static_assert(n < 64, "vmcnt");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0x0070 | (n & 15) | (n >> 4) << 14);   // vmcnt(n) lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    ThinW oa;
+    OZ oz;
+    oa.init(dw.b, dw.ldb, n0, dw.b_outs, dw.b_red, wave, lane);
+    oz.init(dw.a, dw.lda, 0, dw.a_outs, dw.red, wave, lane);
+    const int stages = (dw.red + kBK - 1) / kBK;
+    const int s0 = (int)((int64_t)stages * z / dw.split), s1 = (int)((int64_t)stages * (z + 1) / dw.split);
+    auto issue = [&](int s, int buf) {             // past the share: nothing is read, zeros
+        const bool live = s < s1;
+        const int left = live ? dw.red - s * kBK : 0;
+        const uint32_t dst = lds0 + buf * kStage;
+        const uint16_t* from = oz.base + s * oz.step();
+        const auto zh = oz.stage(from, left, live), zl = oz.stage(from + dw.a_part, left, live && dw.parts == 2);
+        const auto aa = oa.stage(oa.base + s * oa.step(), left, live);
+#pragma unroll
+        for (int i = 0; i < OZ::kLoads; ++i) {
+            oz.load(zh, i, left, dst + ThinW::kBytes, wave);
+            oz.load(zl, i, left, dst + ThinW::kBytes + OZ::kBytes, wave);
+        }
+#pragma unroll
+        for (int i = 0; i < ThinW::kLoads; ++i) oa.load(aa, i, left, dst, wave);
+    };
+    constexpr int TN = NO / 16;
+    typename ThinW::template Reader<4> ra;
+    typename OZ::template Reader<TN> rz;
+    ra.init(wave * 64, lane);
+    rz.init(0, lane);
+    f32x4 sum[TN][4];
+#pragma unroll
+    for (int f = 0; f < TN; ++f)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int col = n0 + wave * 64 + (lane >> 4) * 8;
+    issue(s0, 0);
+    thin_load(da, n0, lds0 + kStage, wave, lane);              // w passes through the other buffer
+    sync(std::integral_constant<int, 0>{});
+    s16x8 w[NO / 32][4];
+    thin_weights(lds + kStage, wave, lane, w);
+    sync(std::integral_constant<int, 0>{});
+    issue(s0 + 1, 1);
+    for (int s = s0; s < s1; ++s) {
+        const int buf = (s - s0) & 1;
+        const char* base = lds + buf * kStage;
+        const char* zbase = base + ThinW::kBytes;
+        sync(std::integral_constant<int, 1>{});
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            s16x8 fa[4], fz[2][TN];
+#pragma unroll
+            for (int f = 0; f < TN; ++f) {
+                fz[0][f] = rz.read(zbase, f, ks);
+                fz[1][f] = rz.read(zbase + OZ::kBytes, f, ks);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) fa[j] = ra.read(base, j, ks);
+#pragma unroll
+            for (int f = 0; f < TN; ++f)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    sum[f][j] = mfma_dt<DT>(fa[j], fz[0][f], sum[f][j]);
+                    if (dw.parts == 2) sum[f][j] = mfma_dt<DT>(fa[j], fz[1][f], sum[f][j]);
+                }
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {                          // 16 rows of da
+            const int r = g * 16 + (lane & 15);
+            const uint32_t sw = ((r & 3) | (((r >> 3) & 3) << 2)) & OZ::kPairMask;
+            s16x8 zr[2][NO / 32];
+#pragma unroll
+            for (int h = 0; h < NO / 32; ++h) {
+                const uint32_t c = h * 4 + (lane >> 4);
+                const char* q = zbase + r * (NO * 2) + (((c >> 1) ^ sw) << 5) + (c & 1) * 16;
+                zr[0][h] = *(const s16x8*)q;
+                zr[1][h] = *(const s16x8*)(q + OZ::kBytes);
+            }
+            f32x4 acc[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < NO / 32; ++h) acc[j] = mfma_dt<DT>(w[h][j], zr[0][h], acc[j]);
+                if (dw.parts == 2) {
+#pragma unroll
+                    for (int h = 0; h < NO / 32; ++h) acc[j] = mfma_dt<DT>(w[h][j], zr[1][h], acc[j]);
+                }
+            }
+            const int64_t row = (int64_t)s * kBK + r;
+            if (row < da.M) thin_store<DT>(da, acc, row, col);
+        }
+        // every wave is done with the buffer; the stores count as older than the loads to come
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0xc07f);                    // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        issue(s + 2, buf);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0070);                        // nothing may land in LDS any more
+#pragma unroll
+    for (int f = 0; f < TN; ++f) {
+        const int n = f * 16 + (lane & 15);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = n0 + wave * 64 + j * 16 + 4 * (lane >> 4);
+            if (n < dw.M && c < dw.ldpart)
+                *(f32x4*)(dw.part + ((int64_t)z * dw.M + n) * dw.ldpart + c) = sum[f][j];
+        }
     }
 #endif
 }
@@ -332,11 +485,25 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(LinearProduct p) {
         const int col = (int)(i - row * n8) * 8;
         const float* src = p.part + row * p.ldpart + col;
         f32x4 lo = *(const f32x4*)src, hi = *(const f32x4*)(src + 4);
+        const int64_t part = (int64_t)p.M * p.ldpart;
+        int z = 1;
+        for (; z + 15 <= p.split; z += 15) {                   // as many on their way at once
+            f32x4 l[15], h[15];
+#pragma unroll
+            for (int i = 0; i < 15; ++i) {
+                l[i] = *(const f32x4*)(src + (z + i) * part);
+                h[i] = *(const f32x4*)(src + (z + i) * part + 4);
+            }
+#pragma unroll
+            for (int i = 0; i < 15; ++i) {
+                lo += l[i];
+                hi += h[i];
+            }
+        }
 #pragma unroll 4
-        for (int z = 1; z < p.split; ++z) {
-            const float* sz = src + (int64_t)z * p.M * p.ldpart;
-            lo += *(const f32x4*)sz;
-            hi += *(const f32x4*)(sz + 4);
+        for (; z < p.split; ++z) {
+            lo += *(const f32x4*)(src + z * part);
+            hi += *(const f32x4*)(src + z * part + 4);
         }
         float v[1][8], bias[8];
 #pragma unroll
@@ -533,7 +700,7 @@ __device__ __forceinline__ void dz_rows(const LinearDz& p, int col, int64_t row,
 
 template <int DT>
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinearDz p) {
-    __shared__ float red[256][9];
+    __shared__ float red[256][9], red8[256];
     const int across = 1 << p.lc, down = 256 >> p.lc;
     const int tc = threadIdx.x & (across - 1), tr = threadIdx.x >> p.lc;
     const int col = (blockIdx.x * across + tc) * 8;
@@ -549,14 +716,19 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearDz p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) red[threadIdx.x][i] = sum[i];
     __syncthreads();
-    for (int c = threadIdx.x; c < across * 8; c += 256) {          // rows in order
-        float t = 0.0f;
-        for (int r = 0; r < down; ++r) t += red[(r << p.lc) + (c >> 3)][c & 7];
-        const int n = blockIdx.x * across * 8 + c;
-        if (n >= p.N) continue;
-        if (p.bias) p.bias[n] = f32_to_dt<DT>(t);                  // one block down the rows
-        else p.sums[(int64_t)blockIdx.y * p.N + n] = t;
-    }
+    // eight rows of a column per thread, in order, then these sums in order
+    const int cols = across * 8, c = threadIdx.x & (cols - 1), g = threadIdx.x / cols;
+    float t = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) t += red[((g * 8 + r) << p.lc) + (c >> 3)][c & 7];
+    red8[threadIdx.x] = t;
+    __syncthreads();
+    if (g) return;
+    for (int i = 1; i < down / 8; ++i) t += red8[i * cols + c];
+    const int n = blockIdx.x * cols + c;
+    if (n >= p.N) return;
+    if (p.bias) p.bias[n] = f32_to_dt<DT>(t);                      // one block down the rows
+    else p.sums[(int64_t)blockIdx.y * p.N + n] = t;
 }
 
 // grad_bias from the blocks' column sums: 16 threads per column, each a sixteenth of the blocks,
@@ -611,6 +783,7 @@ constexpr int kCus = 256;
 // 16 x 4096 x 4096 11.4 / 12.5, 16 x 4096 x 6400 20.0 / 15.6 -- and one launch less on the host.
 constexpr int kStream = 100, kThin = 101;            // kThin: linear_thin_kernel
 constexpr int64_t kStreamMost = (int64_t)1 << 28;
+constexpr int kNarrowBlocks = 256;
 
 // Waves per block: about 4096 in all, 4 to 16 a block, at most one per stage of K.
 template <int DT>
@@ -749,6 +922,35 @@ hipError_t launch_linear_pair(const LinearProduct& da, const LinearProduct& dw, 
     const int grid = (da.whole + 7) / 8 * 8 + dw.whole;
     if (dtype == MOE_DT_BF16) linear_pair_kernel<MOE_DT_BF16><<<grid, 512, 0, s>>>(da, dw);
     else linear_pair_kernel<MOE_DT_FP16><<<grid, 512, 0, s>>>(da, dw);
+    return hipGetLastError();
+}
+
+// The gradients of a narrow layer as one pass: up to 256 blocks (512 blocks: 8192 x 4096 x 64 50
+// against 43 us), a share of at least two stages each.  Not for small layers, whose two launches are as
+// soon done (both gradients, us, one pass against two launches: 4096 x 2048 x 60 28.6 / 27.0, 8192 x 2048 x
+// 16 26.7 / 25.8, 2048 x 4096 x 16 from fp32 20.2 / 22.8, 65536 x 2048 x 64 137 / 195).
+int linear_narrow_split(int M, int K) {
+    const int stages = (M + kBK - 1) / kBK, wide = (K + 255) / 256;
+    const int want = kNarrowBlocks / wide, most = stages / 2;
+    const int split = want < most ? want : most;
+    return split > 1 ? split : 1;
+}
+size_t linear_narrow_bytes(const LinearProduct& da, const LinearProduct& dw) {
+    if (da.cfg != kThin || (int64_t)da.M * da.N < (dw.M <= 32 ? 1 << 23 : 1 << 24)) return 0;
+    return (size_t)linear_narrow_split(da.M, da.N) * dw.M * ((dw.N + 7) / 8 * 8) * 4;
+}
+hipError_t launch_linear_narrow(const LinearProduct& da, LinearProduct dw, int dtype, hipStream_t s) {
+    dw.split = linear_narrow_split(da.M, da.N);
+    dw.ldpart = (dw.N + 7) / 8 * 8;
+    const dim3 grid((da.N + 255) / 256, dw.split);
+    auto go = [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        if (dw.M <= 32) linear_narrow_kernel<DT, 32><<<grid, 256, 0, s>>>(da, dw);
+        else linear_narrow_kernel<DT, 64><<<grid, 256, 0, s>>>(da, dw);
+        linear_reduce_kernel<DT><<<grid_for((int64_t)dw.M * (dw.ldpart / 8), 256), 256, 0, s>>>(dw);
+    };
+    if (dtype == MOE_DT_BF16) go(std::integral_constant<int, MOE_DT_BF16>{});
+    else go(std::integral_constant<int, MOE_DT_FP16>{});
     return hipGetLastError();
 }
 

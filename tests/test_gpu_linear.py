@@ -292,6 +292,31 @@ def test_linear_backward_strided_rows(pads, act):
         _check_backward(M, K, N, "fp16", act=act, pads=pads)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,K,N", [(64, 140000, 1), (65, 262144, 33), (150, 70001, 32), (66000, 128, 31),
+                                   (17001, 1000, 64), (4229, 1000, 64)])
+def test_linear_backward_narrow(M, K, N, dtype):
+    """Layers of up to 64 outputs, both gradients in one pass over the rows and the input's alone:
+    shares of one stage, rows and columns that end inside one, strides, two parts, the same bits twice."""
+    import torch
+    for grad, act, pads in (("same", "none", (0, 0, 0, 0)), ("fp32", "relu", (5, 3, 1, 2)),
+                            ("same", "silu", (8, 16, 8, 8))):
+        case(f"linear backward narrow {M}x{K}x{N} {dtype} {grad} {act} {pads}")
+        _check_backward(M, K, N, dtype, grad=grad, act=act, pads=pads)
+        _check_backward(M, K, N, dtype, grad=grad, act=act, pads=pads, only=("a",))
+    g = torch.Generator(device="cuda").manual_seed(0)
+    dt = _t(dtype)
+    go, a, w = (_rand(g, s, 1.0, dt) for s in ((M, N), (M, K), (N, K)))
+    first = q.moe_linear_backward(go, a, w)
+    assert all(torch.equal(x, y) for x, y in zip(first, q.moe_linear_backward(go, a, w)))
+    # a row that is not a number reaches its own row of grad_a and all of grad_w, nothing else
+    go[M // 2] = float("nan")
+    ga, gw, gb = q.moe_linear_backward(go, a, w)
+    assert torch.isnan(ga[M // 2]).all() and torch.isnan(gw).all() and torch.isnan(gb).all()
+    ga[M // 2] = first[0][M // 2]
+    assert torch.equal(ga, first[0])
+
+
 @pytest.mark.parametrize("only", [("a",), ("w",), ("bias",), ("a", "bias")])
 def test_linear_backward_wanted_gradients_only(only):
     case(f"linear backward only {only}")
