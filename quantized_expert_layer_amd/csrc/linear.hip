@@ -276,6 +276,8 @@ __device__ __forceinline__ void thin_store(const LinearProduct& p, const f32x4 (
                             acc[2 * c + 1][0], acc[2 * c + 1][1], acc[2 * c + 1][2], acc[2 * c + 1][3]};
         if (p.epi.vec && col + 32 * c + 8 <= p.N) {
             *(u32x4*)(dst + 32 * c) = pack16<DT>(v);
+        } else if (col + 32 * c + 8 <= p.N) {
+            store_piece(dst + 32 * c, pack16<DT>(v));
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)

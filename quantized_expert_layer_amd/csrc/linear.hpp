@@ -239,6 +239,9 @@ __device__ __forceinline__ u32x4 pack16(const float (&v)[8]) {
         o[h] = f32_to_dt<DT>(v[2 * h]) | (uint32_t)f32_to_dt<DT>(v[2 * h + 1]) << 16;
     return o;
 }
+// 16 bytes of a row that starts on 2 (an odd row length).
+__device__ __forceinline__ void store_piece(uint16_t* dst, const u32x4& v) { __builtin_memcpy(dst, &v, 16); }
+
 template <int DT>
 __device__ __forceinline__ void load_bias(const LinearEpilogue& e, int col, int n, float (&b)[8]) {
 #pragma unroll
@@ -257,7 +260,7 @@ __device__ __forceinline__ void linear_epilogue(const LinearEpilogue& e, float (
                                                 const float (&bias)[8], int64_t row0, int step,
                                                 int m, int col, int n) {
     const int live = min(8, n - col);                   // columns of this lane, may be <= 0
-    const bool vec = live == 8 && e.vec;                // rows of 16-byte pieces throughout
+    const bool vec = live == 8 && e.vec;                // 16-byte aligned pieces throughout
     bool ok[R];
     u32x4 res[R];
 #pragma unroll
@@ -279,6 +282,8 @@ __device__ __forceinline__ void linear_epilogue(const LinearEpilogue& e, float (
             uint16_t* dst = e.preact + (row0 + r * step) * e.ldp + col;
             if (vec) {
                 *(u32x4*)dst = pack16<DT>(v[r]);
+            } else if (live == 8) {
+                store_piece(dst, pack16<DT>(v[r]));
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -310,6 +315,11 @@ __device__ __forceinline__ void linear_epilogue(const LinearEpilogue& e, float (
             if (vec) {
                 *(f32x4*)dst = f32x4{v[r][0], v[r][1], v[r][2], v[r][3]};
                 *(f32x4*)(dst + 4) = f32x4{v[r][4], v[r][5], v[r][6], v[r][7]};
+            } else if (live == 8) {
+                const f32x4 lo = {v[r][0], v[r][1], v[r][2], v[r][3]};
+                const f32x4 hi = {v[r][4], v[r][5], v[r][6], v[r][7]};
+                __builtin_memcpy(dst, &lo, 16);
+                __builtin_memcpy(dst + 4, &hi, 16);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -319,6 +329,8 @@ __device__ __forceinline__ void linear_epilogue(const LinearEpilogue& e, float (
             uint16_t* dst = (uint16_t*)e.out + (row0 + r * step) * e.ldo + col;
             if (vec) {
                 *(u32x4*)dst = pack16<DT>(v[r]);
+            } else if (live == 8) {
+                store_piece(dst, pack16<DT>(v[r]));
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
