@@ -827,6 +827,7 @@ int32_t moe_linear_backward(const void* grad_out, int64_t ldg, int32_t grad_dtyp
     if (c.used && (!ws || ws_bytes < c.used || !aligned(ws, 16))) return MOE_ERR_WORKSPACE;
     if (int32_t st = check_device()) return st;
     hipStream_t s = (hipStream_t)stream;
+    moe::LinearBias bias{};
     if (N > 0 && (f.need_dz || grad_bias)) {
         moe::LinearDz& z = f.dz;
         z.grad = grad_out;
@@ -840,7 +841,7 @@ int32_t moe_linear_backward(const void* grad_out, int64_t ldg, int32_t grad_dtyp
         z.N = N;
         if (!grad_a && !grad_w) z.dz = nullptr;
         if (!grad_bias) z.sums = nullptr;
-        if (moe::launch_linear_dz(z, dtype, grad_bias, s) != hipSuccess) return MOE_ERR_HIP;
+        if (moe::launch_linear_dz(z, dtype, grad_bias, bias, s) != hipSuccess) return MOE_ERR_HIP;
     }
     const uint16_t* dz = f.need_dz ? f.dz.dz : (const uint16_t*)grad_out;
     const bool want_a = grad_a && M > 0, want_w = grad_w && N > 0;
@@ -854,10 +855,11 @@ int32_t moe_linear_backward(const void* grad_out, int64_t ldg, int32_t grad_dtyp
     grad_out_epilogue(f.dw.epi, grad_w, K);
     if (want_a && want_w && f.narrow) {
         f.dw.part = f.part;
-        return hip_status(moe::launch_linear_narrow(f.da, f.dw, dtype, s));
+        return hip_status(moe::launch_linear_narrow(f.da, f.dw, bias, dtype, s));
     }
     if (want_a && want_w && moe::linear_pair(f.da, f.dw))
-        return hip_status(moe::launch_linear_pair(f.da, f.dw, dtype, s));
+        return hip_status(moe::launch_linear_pair(f.da, f.dw, bias, dtype, s));
+    if (moe::launch_linear_bias(bias, dtype, s) != hipSuccess) return MOE_ERR_HIP;
     if (want_a && moe::launch_linear_product(f.da, dtype, s) != hipSuccess) return MOE_ERR_HIP;
     if (want_w && moe::launch_linear_product(f.dw, dtype, s) != hipSuccess) return MOE_ERR_HIP;
     return MOE_OK;

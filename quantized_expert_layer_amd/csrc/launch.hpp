@@ -181,21 +181,31 @@ struct LinearDz {
     uint16_t* bias;          // grad_bias where one block sums all rows, else NULL (set by the launch)
 };
 
+struct LinearBias {          // what is left to do for grad_bias after linear_dz (out NULL: nothing)
+    const float* sums;       // [blocks, N]
+    int blocks, N;
+    uint16_t* out;
+};
+
 // Chooses tile, split and the partial layout from the sizes (host-only, deterministic).
 void linear_plan(LinearProduct& p);
 size_t linear_part_bytes(const LinearProduct& p);
 hipError_t launch_linear_product(const LinearProduct& p, int dtype, hipStream_t stream);
 // Both gradients in one launch, if that is the better plan for them (which it then becomes).
 bool linear_pair(LinearProduct& da, LinearProduct& dw);
-hipError_t launch_linear_pair(const LinearProduct& da, const LinearProduct& dw, int dtype,
-                              hipStream_t stream);
+hipError_t launch_linear_pair(const LinearProduct& da, const LinearProduct& dw, const LinearBias& b,
+                              int dtype, hipStream_t stream);
 // Both gradients of a narrow layer (its input gradient's plan is the narrow one) in one pass;
 // dw.part holds linear_narrow_bytes.
 size_t linear_narrow_bytes(const LinearProduct& da, const LinearProduct& dw);
-hipError_t launch_linear_narrow(const LinearProduct& da, LinearProduct dw, int dtype, hipStream_t stream);
+hipError_t launch_linear_narrow(const LinearProduct& da, LinearProduct dw, const LinearBias& b,
+                                int dtype, hipStream_t stream);
 hipError_t launch_linear_pack(const LinearPack& a, const LinearPack& b, hipStream_t stream);
 int linear_dz_blocks(int M, int N);
-hipError_t launch_linear_dz(const LinearDz& p, int dtype, uint16_t* grad_bias, hipStream_t stream);
+// grad_bias is written here, or what is left of it goes to `rest`, for a later launch.
+hipError_t launch_linear_dz(const LinearDz& p, int dtype, uint16_t* grad_bias, LinearBias& rest,
+                            hipStream_t stream);
+hipError_t launch_linear_bias(const LinearBias& b, int dtype, hipStream_t stream);
 
 // ---- balance loss and the router's gradients ----
 struct BalanceParams {

@@ -213,10 +213,36 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearProduct
     tile_body<DT, ACOLS, BCOLS, BM, BN, WM, WN, NBUF>(p, lds, z, tm * BM, tn * BN);
 }
 
-// Both gradients' products in one launch, 128 x 128 tiles, two blocks per CU: each alone leaves the
-// chip half empty where neither fills it (3777 x 1024 x 4096 fp16: 39 + 41 us one after the other).
+// grad_bias of 64 columns from the dz blocks' column sums: a block's G groups of 64 threads take
+// every G-th of them, and are then added in order.
+template <int DT, int G>
+__device__ __forceinline__ void bias_body(const LinearBias& b, int block, float (*red)[64]) {
+    const int lane = threadIdx.x & 63, g = threadIdx.x / 64;
+    const int col = block * 64 + lane;
+    float v = 0.0f;
+    if (col < b.N) {
+#pragma unroll 8
+        for (int i = g; i < b.blocks; i += G) v += b.sums[(int64_t)i * b.N + col];
+    }
+    red[g][lane] = v;
+    __syncthreads();
+    if (g == 0 && col < b.N) {
+#pragma unroll
+        for (int i = 1; i < G; ++i) v += red[i][lane];
+        b.out[col] = f32_to_dt<DT>(v);
+    }
+}
 template <int DT>
-__global__ __launch_bounds__(512) void linear_pair_kernel(LinearProduct da, LinearProduct dw) {
+__global__ __launch_bounds__(1024) void linear_bias_kernel(LinearBias b) {
+    __shared__ float red[16][64];
+    bias_body<DT, 16>(b, blockIdx.x, red);
+}
+
+// Both gradients' products in one launch, 128 x 128 tiles, two blocks per CU: each alone leaves the
+// chip half empty where neither fills it (3777 x 1024 x 4096 fp16: 39 + 41 us one after the other, 68
+// together).  The last blocks finish the bias gradient.
+template <int DT>
+__global__ __launch_bounds__(512) void linear_pair_kernel(LinearProduct da, LinearProduct dw, LinearBias b) {
     __shared__ __attribute__((aligned(1024))) char lds[(128 + 128) * kBK * 2 * 2];
     const int na = (da.whole + 7) / 8 * 8;                     // keeps dw's blocks on their XCDs
     int tm, tn;
@@ -224,9 +250,11 @@ __global__ __launch_bounds__(512) void linear_pair_kernel(LinearProduct da, Line
         if ((int)blockIdx.x >= da.whole) return;
         tile_of(da, blockIdx.x, da.whole, tm, tn);
         tile_body<DT, false, true, 128, 128, 2, 4, 2>(da, lds, 0, tm * 128, tn * 128);
-    } else {
+    } else if ((int)blockIdx.x < na + dw.whole) {
         tile_of(dw, blockIdx.x - na, dw.whole, tm, tn);
         tile_body<DT, true, true, 128, 128, 2, 4, 2>(dw, lds, 0, tm * 128, tn * 128);
+    } else {
+        bias_body<DT, 8>(b, blockIdx.x - na - dw.whole, (float(*)[64])lds);
     }
 }
 
@@ -477,12 +505,18 @@ __global__ __launch_bounds__(256) void linear_narrow_kernel(LinearProduct da, Li
 #endif
 }
 
-// Sums the splits' partial products in their order and applies the epilogue.
+// Sums the splits' partial products in their order and applies the epilogue; the blocks past the
+// first `blocks` finish a bias gradient.
 template <int DT>
-__global__ __launch_bounds__(256) void linear_reduce_kernel(LinearProduct p) {
+__global__ __launch_bounds__(256) void linear_reduce_kernel(LinearProduct p, int blocks, LinearBias b) {
+    __shared__ float red[4][64];
+    if ((int)blockIdx.x >= blocks) {
+        bias_body<DT, 4>(b, blockIdx.x - blocks, red);
+        return;
+    }
     const int n8 = p.ldpart / 8;
     const int64_t total = (int64_t)p.M * n8;
-    for (int64_t i = blockIdx.x * 256 + (int64_t)threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    for (int64_t i = blockIdx.x * 256 + (int64_t)threadIdx.x; i < total; i += (int64_t)blocks * 256) {
         const int64_t row = i / n8;
         const int col = (int)(i - row * n8) * 8;
         const float* src = p.part + row * p.ldpart + col;
@@ -733,27 +767,6 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearDz p) {
     else p.sums[(int64_t)blockIdx.y * p.N + n] = t;
 }
 
-// grad_bias from the blocks' column sums: 16 threads per column, each a sixteenth of the blocks,
-// added in order.
-template <int DT>
-__global__ __launch_bounds__(1024) void linear_bias_kernel(const float* __restrict__ sums, int blocks,
-                                                           int N, uint16_t* __restrict__ out) {
-    __shared__ float red[16][64];
-    const int lane = threadIdx.x & 63, g = threadIdx.x / 64;
-    const int col = blockIdx.x * 64 + lane;
-    float v = 0.0f;
-    if (col < N) {
-#pragma unroll 8
-        for (int b = g; b < blocks; b += 16) v += sums[(int64_t)b * N + col];
-    }
-    red[g][lane] = v;
-    __syncthreads();
-    if (g == 0 && col < N) {
-        for (int i = 1; i < 16; ++i) v += red[i][lane];
-        out[col] = f32_to_dt<DT>(v);
-    }
-}
-
 // ------------------------------------------------------------------------------------ host
 namespace {
 
@@ -805,6 +818,14 @@ void launch_thin(const LinearProduct& p, hipStream_t s) {
     int64_t rows = ((int64_t)p.M * wide / 1024 + 63) / 64 * 64;
     rows = rows < 64 ? 64 : rows > 1 << 15 ? 1 << 15 : rows;
     linear_thin_kernel<DT><<<dim3(wide, (unsigned)((p.M + rows - 1) / rows)), 256, 0, s>>>(p, (int)rows);
+}
+
+int bias_blocks(const LinearBias& b) { return b.out ? (b.N + 63) / 64 : 0; }
+
+template <int DT>
+void launch_reduce(const LinearProduct& p, const LinearBias& b, hipStream_t s) {
+    const int blocks = grid_for((int64_t)p.M * (p.ldpart / 8), 256);
+    linear_reduce_kernel<DT><<<blocks + bias_blocks(b), 256, 0, s>>>(p, blocks, b);
 }
 
 template <int DT, bool AC, bool BC>
@@ -888,8 +909,7 @@ hipError_t launch_linear_product(const LinearProduct& p, int dtype, hipStream_t 
         else if (!p.a_cols && !p.b_cols) launch_tiles<DT, false, false>(p, s);
         else if (!p.a_cols) launch_tiles<DT, false, true>(p, s);
         else launch_tiles<DT, true, true>(p, s);
-        if (p.split > 1)
-            linear_reduce_kernel<DT><<<grid_for((int64_t)p.M * (p.ldpart / 8), 256), 256, 0, s>>>(p);
+        if (p.split > 1) launch_reduce<DT>(p, LinearBias{}, s);
     };
     if (dtype == MOE_DT_BF16) go(std::integral_constant<int, MOE_DT_BF16>{});
     else go(std::integral_constant<int, MOE_DT_FP16>{});
@@ -919,11 +939,11 @@ bool linear_pair(LinearProduct& da, LinearProduct& dw) {
     return true;
 }
 
-hipError_t launch_linear_pair(const LinearProduct& da, const LinearProduct& dw, int dtype,
-                              hipStream_t s) {
-    const int grid = (da.whole + 7) / 8 * 8 + dw.whole;
-    if (dtype == MOE_DT_BF16) linear_pair_kernel<MOE_DT_BF16><<<grid, 512, 0, s>>>(da, dw);
-    else linear_pair_kernel<MOE_DT_FP16><<<grid, 512, 0, s>>>(da, dw);
+hipError_t launch_linear_pair(const LinearProduct& da, const LinearProduct& dw, const LinearBias& b,
+                              int dtype, hipStream_t s) {
+    const int grid = (da.whole + 7) / 8 * 8 + dw.whole + bias_blocks(b);
+    if (dtype == MOE_DT_BF16) linear_pair_kernel<MOE_DT_BF16><<<grid, 512, 0, s>>>(da, dw, b);
+    else linear_pair_kernel<MOE_DT_FP16><<<grid, 512, 0, s>>>(da, dw, b);
     return hipGetLastError();
 }
 
@@ -941,7 +961,8 @@ size_t linear_narrow_bytes(const LinearProduct& da, const LinearProduct& dw) {
     if (da.cfg != kThin || (int64_t)da.M * da.N < (dw.M <= 32 ? 1 << 23 : 1 << 24)) return 0;
     return (size_t)linear_narrow_split(da.M, da.N) * dw.M * ((dw.N + 7) / 8 * 8) * 4;
 }
-hipError_t launch_linear_narrow(const LinearProduct& da, LinearProduct dw, int dtype, hipStream_t s) {
+hipError_t launch_linear_narrow(const LinearProduct& da, LinearProduct dw, const LinearBias& b,
+                                int dtype, hipStream_t s) {
     dw.split = linear_narrow_split(da.M, da.N);
     dw.ldpart = (dw.N + 7) / 8 * 8;
     const dim3 grid((da.N + 255) / 256, dw.split);
@@ -949,7 +970,7 @@ hipError_t launch_linear_narrow(const LinearProduct& da, LinearProduct dw, int d
         constexpr int DT = decltype(dt)::value;
         if (dw.M <= 32) linear_narrow_kernel<DT, 32><<<grid, 256, 0, s>>>(da, dw);
         else linear_narrow_kernel<DT, 64><<<grid, 256, 0, s>>>(da, dw);
-        linear_reduce_kernel<DT><<<grid_for((int64_t)dw.M * (dw.ldpart / 8), 256), 256, 0, s>>>(dw);
+        launch_reduce<DT>(dw, b, s);
     };
     if (dtype == MOE_DT_BF16) go(std::integral_constant<int, MOE_DT_BF16>{});
     else go(std::integral_constant<int, MOE_DT_FP16>{});
@@ -980,20 +1001,23 @@ int linear_dz_blocks(int M, int N) {
     return (int)(rows <= 4 ? 1 : rows < want ? rows : want);
 }
 
-hipError_t launch_linear_dz(const LinearDz& args, int dtype, uint16_t* grad_bias, hipStream_t s) {
+hipError_t launch_linear_bias(const LinearBias& b, int dtype, hipStream_t s) {
+    if (!b.out) return hipSuccess;
+    if (dtype == MOE_DT_BF16) linear_bias_kernel<MOE_DT_BF16><<<bias_blocks(b), 1024, 0, s>>>(b);
+    else linear_bias_kernel<MOE_DT_FP16><<<bias_blocks(b), 1024, 0, s>>>(b);
+    return hipGetLastError();
+}
+
+hipError_t launch_linear_dz(const LinearDz& args, int dtype, uint16_t* grad_bias, LinearBias& rest,
+                            hipStream_t s) {
     LinearDz p = args;
     p.lc = dz_across(p.N);
     const int blocks = linear_dz_blocks(p.M, p.N);
     p.bias = blocks == 1 ? grad_bias : nullptr;
     const dim3 grid((p.cols8 / 8 + (1 << p.lc) - 1) >> p.lc, blocks);
-    auto go = [&](auto dt) {
-        constexpr int DT = decltype(dt)::value;
-        linear_dz_kernel<DT><<<grid, 256, 0, s>>>(p);
-        if (grad_bias && blocks > 1)
-            linear_bias_kernel<DT><<<(p.N + 63) / 64, 1024, 0, s>>>(p.sums, blocks, p.N, grad_bias);
-    };
-    if (dtype == MOE_DT_BF16) go(std::integral_constant<int, MOE_DT_BF16>{});
-    else go(std::integral_constant<int, MOE_DT_FP16>{});
+    if (grad_bias && blocks > 1) rest = LinearBias{p.sums, blocks, p.N, grad_bias};
+    if (dtype == MOE_DT_BF16) linear_dz_kernel<MOE_DT_BF16><<<grid, 256, 0, s>>>(p);
+    else linear_dz_kernel<MOE_DT_FP16><<<grid, 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
