@@ -184,7 +184,9 @@ __device__ __forceinline__ void tile_body(const LinearProduct& p, char* lds, int
                     }
                 }
             } else {
-                linear_epilogue<DT, RB>(p.epi, v, bias, row0, RPI, p.M, col, p.N);
+                u32x4 res[RB];
+                load_residual(p.epi, res, row0, RPI, p.M, col, p.N);
+                linear_epilogue<DT, RB>(p.epi, v, bias, res, row0, RPI, p.M, col, p.N);
             }
         }
         lds_wave_fence();
@@ -548,7 +550,9 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(LinearProduct p, int
             v[0][c + 4] = hi[c];
         }
         load_bias<DT>(p.epi, col, p.N, bias);
-        linear_epilogue<DT, 1>(p.epi, v, bias, row, 0, p.M, col, p.N);
+        u32x4 res[1];
+        load_residual(p.epi, res, row, 0, p.M, col, p.N);
+        linear_epilogue<DT, 1>(p.epi, v, bias, res, row, 0, p.M, col, p.N);
     }
 }
 
@@ -578,12 +582,16 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(LinearProduct p) {
     const uint32_t wo = (uint32_t)((lane & 15) * ld_b + kl) * 2u;
     const uint32_t ao = (uint32_t)((lane & 15) * ld_a + kl) * 2u;
     const bool w_row = n0 + (lane & 15) < p.b_outs;
-    // the epilogue's thread: row t / 2, eight columns
+    // the epilogue's thread: row t / 2, eight columns, its bias and residual asked for first
     const int t = threadIdx.x, row = t / 2, c8 = (t & 1) * 8;
     const int col = n0 + c8;
     const bool out = row < p.M && row < 16 * MT && col < p.N;
     float v[1][8] = {}, bias[8] = {};
-    if (out) load_bias<DT>(p.epi, col, p.N, bias);
+    u32x4 res[1] = {};
+    if (out) {
+        load_bias<DT>(p.epi, col, p.N, bias);
+        load_residual(p.epi, res, row, 0, p.M, col, p.N);
+    }
     f32x4 acc[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -626,7 +634,7 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(LinearProduct p) {
             v[0][c + 4] += hi[c];
         }
     }
-    linear_epilogue<DT, 1>(p.epi, v, bias, row, 0, p.M, col, p.N);
+    linear_epilogue<DT, 1>(p.epi, v, bias, res, row, 0, p.M, col, p.N);
 #endif
 }
 

@@ -255,20 +255,24 @@ __device__ __forceinline__ void apply_act(float (&v)[R][8]) {
         for (int i = 0; i < 8; ++i) v[r][i] = act_value<ACT>(v[r][i]);
 }
 
+template <int R>
+__device__ __forceinline__ void load_residual(const LinearEpilogue& e, u32x4 (&res)[R], int64_t row0,
+                                              int step, int m, int col, int n) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (e.residual && e.vec && n - col >= 8 && row0 + r * step < m)
+            res[r] = *(const u32x4*)(e.residual + (row0 + r * step) * e.ldr + col);
+}
+// With `res` as load_residual left it.
 template <int DT, int R>
 __device__ __forceinline__ void linear_epilogue(const LinearEpilogue& e, float (&v)[R][8],
-                                                const float (&bias)[8], int64_t row0, int step,
-                                                int m, int col, int n) {
+                                                const float (&bias)[8], const u32x4 (&res)[R],
+                                                int64_t row0, int step, int m, int col, int n) {
     const int live = min(8, n - col);                   // columns of this lane, may be <= 0
     const bool vec = live == 8 && e.vec;                // 16-byte aligned pieces throughout
     bool ok[R];
-    u32x4 res[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        ok[r] = row0 + r * step < m && live > 0;
-        if (e.residual && vec && ok[r])
-            res[r] = *(const u32x4*)(e.residual + (row0 + r * step) * e.ldr + col);
-    }
+    for (int r = 0; r < R; ++r) ok[r] = row0 + r * step < m && live > 0;
     if (e.bias) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
