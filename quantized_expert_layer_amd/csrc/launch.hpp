@@ -140,7 +140,6 @@ struct LinearEpilogue {      // out = act(sum + bias) + residual; preact = sum +
     void* out;               // 16-bit of the operands' type, or fp32
     int64_t ldo;
     int out_f32, act;
-    int vec;                 // eight columns of a row are 16-byte aligned in every matrix here
 };
 
 struct LinearProduct {       // C[i, j] = sum over parts and r < red of A[i, r] B[j, r]
@@ -176,7 +175,6 @@ struct LinearDz {
     uint16_t* dz;            // [parts, M, cols8] or NULL
     int parts;
     float* sums;             // [linear_dz_blocks(M, N), N] or NULL
-    int vec;                 // rows of grad and preact start on 16 bytes
     int lc;                  // log2 of a block's threads across the columns (set by the launch)
     uint16_t* bias;          // grad_bias where one block sums all rows, else NULL (set by the launch)
 };

@@ -304,10 +304,8 @@ __device__ __forceinline__ void thin_store(const LinearProduct& p, const f32x4 (
     for (int c = 0; c < 2; ++c) {
         const float v[8] = {acc[2 * c][0], acc[2 * c][1], acc[2 * c][2], acc[2 * c][3],
                             acc[2 * c + 1][0], acc[2 * c + 1][1], acc[2 * c + 1][2], acc[2 * c + 1][3]};
-        if (p.epi.vec && col + 32 * c + 8 <= p.N) {
-            *(u32x4*)(dst + 32 * c) = pack16<DT>(v);
-        } else if (col + 32 * c + 8 <= p.N) {
-            store_piece(dst + 32 * c, pack16<DT>(v));
+        if (col + 32 * c + 8 <= p.N) {
+            *(u32x4_on2*)(dst + 32 * c) = pack16<DT>(v);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -642,7 +640,6 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(LinearProduct p) {
 // stride not a multiple of 8) into rows of cols8 = cols rounded up to 8, zeros behind; eight values
 // per thread.
 __global__ __launch_bounds__(256) void linear_pack_kernel(LinearPack a, LinearPack b) {
-    struct __attribute__((packed, aligned(2))) Piece { uint32_t v[4]; };   // 16 bytes on 2
     const int64_t na = (int64_t)a.rows * (a.cols8 / 8), nb = (int64_t)b.rows * (b.cols8 / 8);
     for (int64_t j = blockIdx.x * 256 + (int64_t)threadIdx.x; j < na + nb; j += (int64_t)gridDim.x * 256) {
         const LinearPack& m = j < na ? a : b;
@@ -652,9 +649,7 @@ __global__ __launch_bounds__(256) void linear_pack_kernel(LinearPack a, LinearPa
         const uint16_t* s = m.src + r * m.ld + c;
         u32x4 o;
         if (c + 8 <= m.cols) {
-            const Piece q = *(const Piece*)s;
-#pragma unroll
-            for (int h = 0; h < 4; ++h) o[h] = q.v[h];
+            o = *(const u32x4_on2*)s;
         } else {
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
@@ -680,13 +675,13 @@ template <int DT, int ACT>
 __device__ __forceinline__ void dz_rows(const LinearDz& p, int col, int64_t row, int64_t step,
                                         float (&sum)[8]) {
     const int live = min(8, p.N - col);
-    const bool vec = p.vec && live == 8;
+    const bool full = live == 8;                       // 16-byte pieces, on 2 (fp32: on 4) bytes
     for (; row < p.M; row += step) {
         float v[8];
         if (p.grad_f32) {
             const float* src = (const float*)p.grad + row * p.ldg + col;
-            if (vec) {
-                const f32x4 a = *(const f32x4*)src, b = *(const f32x4*)(src + 4);
+            if (full) {
+                const f32x4_on4 a = *(const f32x4_on4*)src, b = *(const f32x4_on4*)(src + 4);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     v[i] = a[i];
@@ -700,8 +695,9 @@ __device__ __forceinline__ void dz_rows(const LinearDz& p, int col, int64_t row,
             const uint16_t* src = (const uint16_t*)p.grad + row * p.ldg + col;
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-            if (vec) {
-                add16<DT>(v, *(const u32x4*)src);
+            if (full) {
+                const u32x4 piece = *(const u32x4_on2*)src;
+                add16<DT>(v, piece);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -711,8 +707,9 @@ __device__ __forceinline__ void dz_rows(const LinearDz& p, int col, int64_t row,
         if constexpr (ACT != MOE_ACT_NONE) {
             const uint16_t* src = p.preact + row * p.ldp + col;
             float z[8] = {};
-            if (vec) {
-                add16<DT>(z, *(const u32x4*)src);
+            if (full) {
+                const u32x4 piece = *(const u32x4_on2*)src;
+                add16<DT>(z, piece);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)

@@ -140,6 +140,26 @@ def test_linear_strided_rows_with_nan_behind_them(pads):
         _check_forward(M, K, N, "bf16", act="relu", pads=pads)
 
 
+@pytest.mark.parametrize("dtype,out", [("fp16", "same"), ("bf16", "same"), ("bf16", "fp32")])
+def test_linear_rows_of_any_length(dtype, out):
+    """Rows that start on 2 (fp32: on 4) bytes, in place too, and nothing written behind them."""
+    import torch
+    for M, K, N in ((20, 96, 61), (130, 200, 259), (300, 64, 1021), (700, 2056, 45)):
+        case(f"linear odd rows {M}x{K}x{N} {dtype}->{out}")
+        _check_forward(M, K, N, dtype, out=out, act="silu", pads=(1, 3, 5, 7, 9))
+        _check_forward(M, K, N, dtype, out=out, act="none", bias=False)
+        if out == "same":
+            _check_forward(M, K, N, dtype, act="relu", inplace=True, pads=(0, 0, 3, 0, 0))
+        g = torch.Generator(device="cuda").manual_seed(N)
+        dt, ot = _t(dtype), _t(dtype if out == "same" else out)
+        x, w = _rand(g, (M, K), 1.0, dt), _rand(g, (N, K), K ** -0.5, dt)
+        buf = torch.full((M, N + 3), 7.0, dtype=ot, device="cuda")
+        kept = torch.full((M, N + 6), 7.0, dtype=dt, device="cuda")
+        q.moe_linear(x, w, act="relu", out=buf[:, :N], preact=kept[:, :N])
+        assert (buf[:, N:] == 7).all() and (kept[:, N:] == 7).all()
+        assert torch.equal(buf[:, :N], q.moe_linear(x, w, act="relu", out_dtype=ot))
+
+
 def test_linear_residual_updated_in_place():
     for M, K, N in ((5, 512, 96), (400, 192, 520)):
         case(f"linear in place {M}x{K}x{N}")
