@@ -731,6 +731,7 @@ moe::LinearPack packed(const uint16_t* src, int64_t ld, int32_t rows, int32_t co
 void grad_out_epilogue(moe::LinearEpilogue& e, uint16_t* out, int32_t K) {
     e.out = out;
     e.ldo = K;
+    e.vec = K % 8 == 0;
 }
 
 }  // namespace
@@ -787,6 +788,7 @@ int32_t moe_linear(const uint16_t* a, int64_t lda, const uint16_t* w, int64_t ld
     e.ldo = ldo;
     e.out_f32 = out_dtype == MOE_DT_FP32;
     e.act = act;
+    e.vec = ldo % 8 == 0 && (!residual || ldr % 8 == 0) && (!preact || ldp % 8 == 0);
     return hip_status(moe::launch_linear_product(p, dtype, s));
 }
 

@@ -140,6 +140,7 @@ struct LinearEpilogue {      // out = act(sum + bias) + residual; preact = sum +
     void* out;               // 16-bit of the operands' type, or fp32
     int64_t ldo;
     int out_f32, act;
+    int vec;                 // eight columns of a row are 16-byte aligned in every matrix here
 };
 
 struct LinearProduct {       // C[i, j] = sum over parts and r < red of A[i, r] B[j, r]

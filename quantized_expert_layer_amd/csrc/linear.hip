@@ -184,9 +184,7 @@ __device__ __forceinline__ void tile_body(const LinearProduct& p, char* lds, int
                     }
                 }
             } else {
-                u32x4 res[RB];
-                load_residual(p.epi, res, row0, RPI, p.M, col, p.N);
-                linear_epilogue<DT, RB>(p.epi, v, bias, res, row0, RPI, p.M, col, p.N);
+                linear_epilogue<DT, RB>(p.epi, v, bias, row0, RPI, p.M, col, p.N);
             }
         }
         lds_wave_fence();
@@ -304,8 +302,10 @@ __device__ __forceinline__ void thin_store(const LinearProduct& p, const f32x4 (
     for (int c = 0; c < 2; ++c) {
         const float v[8] = {acc[2 * c][0], acc[2 * c][1], acc[2 * c][2], acc[2 * c][3],
                             acc[2 * c + 1][0], acc[2 * c + 1][1], acc[2 * c + 1][2], acc[2 * c + 1][3]};
-        if (col + 32 * c + 8 <= p.N) {
-            *(u32x4_on2*)(dst + 32 * c) = pack16<DT>(v);
+        if (p.epi.vec && col + 32 * c + 8 <= p.N) {
+            *(u32x4*)(dst + 32 * c) = pack16<DT>(v);
+        } else if (col + 32 * c + 8 <= p.N) {
+            store_piece(dst + 32 * c, pack16<DT>(v));
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -548,9 +548,7 @@ __global__ __launch_bounds__(256) void linear_reduce_kernel(LinearProduct p, int
             v[0][c + 4] = hi[c];
         }
         load_bias<DT>(p.epi, col, p.N, bias);
-        u32x4 res[1];
-        load_residual(p.epi, res, row, 0, p.M, col, p.N);
-        linear_epilogue<DT, 1>(p.epi, v, bias, res, row, 0, p.M, col, p.N);
+        linear_epilogue<DT, 1>(p.epi, v, bias, row, 0, p.M, col, p.N);
     }
 }
 
@@ -580,16 +578,12 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(LinearProduct p) {
     const uint32_t wo = (uint32_t)((lane & 15) * ld_b + kl) * 2u;
     const uint32_t ao = (uint32_t)((lane & 15) * ld_a + kl) * 2u;
     const bool w_row = n0 + (lane & 15) < p.b_outs;
-    // the epilogue's thread: row t / 2, eight columns, its bias and residual asked for first
+    // the epilogue's thread: row t / 2, eight columns
     const int t = threadIdx.x, row = t / 2, c8 = (t & 1) * 8;
     const int col = n0 + c8;
     const bool out = row < p.M && row < 16 * MT && col < p.N;
     float v[1][8] = {}, bias[8] = {};
-    u32x4 res[1] = {};
-    if (out) {
-        load_bias<DT>(p.epi, col, p.N, bias);
-        load_residual(p.epi, res, row, 0, p.M, col, p.N);
-    }
+    if (out) load_bias<DT>(p.epi, col, p.N, bias);
     f32x4 acc[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -632,7 +626,7 @@ __global__ __launch_bounds__(1024) void linear_stream_kernel(LinearProduct p) {
             v[0][c + 4] += hi[c];
         }
     }
-    linear_epilogue<DT, 1>(p.epi, v, bias, res, row, 0, p.M, col, p.N);
+    linear_epilogue<DT, 1>(p.epi, v, bias, row, 0, p.M, col, p.N);
 #endif
 }
 

@@ -242,6 +242,9 @@ __device__ __forceinline__ u32x4 pack16(const float (&v)[8]) {
         o[h] = f32_to_dt<DT>(v[2 * h]) | (uint32_t)f32_to_dt<DT>(v[2 * h + 1]) << 16;
     return o;
 }
+// 16 bytes of a row that starts on 2 (an odd row length).
+__device__ __forceinline__ void store_piece(uint16_t* dst, const u32x4& v) { *(u32x4_on2*)dst = v; }
+
 template <int DT>
 __device__ __forceinline__ void load_bias(const LinearEpilogue& e, int col, int n, float (&b)[8]) {
 #pragma unroll
@@ -255,23 +258,20 @@ __device__ __forceinline__ void apply_act(float (&v)[R][8]) {
         for (int i = 0; i < 8; ++i) v[r][i] = act_value<ACT>(v[r][i]);
 }
 
-template <int R>
-__device__ __forceinline__ void load_residual(const LinearEpilogue& e, u32x4 (&res)[R], int64_t row0,
-                                              int step, int m, int col, int n) {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (e.residual && n - col >= 8 && row0 + r * step < m)
-            res[r] = *(const u32x4_on2*)(e.residual + (row0 + r * step) * e.ldr + col);
-}
-// With `res` as load_residual left it.
 template <int DT, int R>
 __device__ __forceinline__ void linear_epilogue(const LinearEpilogue& e, float (&v)[R][8],
-                                                const float (&bias)[8], const u32x4 (&res)[R],
-                                                int64_t row0, int step, int m, int col, int n) {
+                                                const float (&bias)[8], int64_t row0, int step,
+                                                int m, int col, int n) {
     const int live = min(8, n - col);                   // columns of this lane, may be <= 0
+    const bool vec = live == 8 && e.vec;                // 16-byte aligned pieces throughout
     bool ok[R];
+    u32x4 res[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) ok[r] = row0 + r * step < m && live > 0;
+    for (int r = 0; r < R; ++r) {
+        ok[r] = row0 + r * step < m && live > 0;
+        if (e.residual && vec && ok[r])
+            res[r] = *(const u32x4*)(e.residual + (row0 + r * step) * e.ldr + col);
+    }
     if (e.bias) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -283,8 +283,10 @@ __device__ __forceinline__ void linear_epilogue(const LinearEpilogue& e, float (
         for (int r = 0; r < R; ++r) {
             if (!ok[r]) continue;
             uint16_t* dst = e.preact + (row0 + r * step) * e.ldp + col;
-            if (live == 8) {
-                *(u32x4_on2*)dst = pack16<DT>(v[r]);
+            if (vec) {
+                *(u32x4*)dst = pack16<DT>(v[r]);
+            } else if (live == 8) {
+                store_piece(dst, pack16<DT>(v[r]));
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -298,15 +300,13 @@ __device__ __forceinline__ void linear_epilogue(const LinearEpilogue& e, float (
     if (e.residual) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (live == 8) {
+            if (vec) {
                 if (ok[r]) add16<DT>(v[r], res[r]);
-            } else if (ok[r]) {                         // without a branch per value: those put v in LDS
+            } else if (ok[r]) {
                 const uint16_t* src = e.residual + (row0 + r * step) * e.ldr + col;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float x = dt_to_f32<DT>(src[min(i, live - 1)]);
-                    v[r][i] += i < live ? x : 0.0f;
-                }
+                for (int i = 0; i < 8; ++i)
+                    if (i < live) v[r][i] += dt_to_f32<DT>(src[i]);
             }
         }
     }
@@ -315,7 +315,10 @@ __device__ __forceinline__ void linear_epilogue(const LinearEpilogue& e, float (
         if (!ok[r]) continue;
         if (e.out_f32) {
             float* dst = (float*)e.out + (row0 + r * step) * e.ldo + col;
-            if (live == 8) {
+            if (vec) {
+                *(f32x4*)dst = f32x4{v[r][0], v[r][1], v[r][2], v[r][3]};
+                *(f32x4*)(dst + 4) = f32x4{v[r][4], v[r][5], v[r][6], v[r][7]};
+            } else if (live == 8) {
                 *(f32x4_on4*)dst = f32x4{v[r][0], v[r][1], v[r][2], v[r][3]};
                 *(f32x4_on4*)(dst + 4) = f32x4{v[r][4], v[r][5], v[r][6], v[r][7]};
             } else {
@@ -325,8 +328,10 @@ __device__ __forceinline__ void linear_epilogue(const LinearEpilogue& e, float (
             }
         } else {
             uint16_t* dst = (uint16_t*)e.out + (row0 + r * step) * e.ldo + col;
-            if (live == 8) {
-                *(u32x4_on2*)dst = pack16<DT>(v[r]);
+            if (vec) {
+                *(u32x4*)dst = pack16<DT>(v[r]);
+            } else if (live == 8) {
+                store_piece(dst, pack16<DT>(v[r]));
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
